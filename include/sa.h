@@ -85,6 +85,8 @@ typedef enum { SA_DTYPE_F32 = 0, SA_DTYPE_BF16 = 1 } sa_dtype;
  *   page_table  int32 [batch][max_pages_per_seq]: logical page -> physical page.
  *   seq_lens    int32 [batch]: tokens of each sequence (<= max_pages_per_seq *
  *               page_size; larger values are clamped and recorded as a fault).
+ * sa_rope_append writes k and v; every other entry point only reads them.
+ * sa_select_blocks(SA_SEL_SPANS) reads neither: both may be NULL there.
  * Slots of a page past seq_len must hold finite values (the prefill tensor-core
  * product multiplies them by an exact zero weight).
  * Supported: head_dim in {64, 128} (prefill: 128), page_size in {16, 64}
@@ -388,6 +390,189 @@ SA_API sa_status sa_tier_plan(int32_t *slot_of, int64_t host_pages, int32_t *pag
 /* int32 words of scratch sa_tier_plan needs: 1 + host_pages + 4 * slots (0 if
  * either argument is < 1). */
 SA_API int64_t sa_tier_plan_scratch_ints(int64_t host_pages, int32_t slots);
+
+/* ------------------------------------------------------------------------ */
+/* 6. sa_plan_append -- pages, positions and slots of a step                */
+/* ------------------------------------------------------------------------ */
+/*
+ * [DA-1] (DA state machine section: the KV cache is kept in fixed-size blocks
+ * named by a table).  The device keeps the page tables, the lengths and a
+ * stack of free pages; one call turns the number of new tokens of every
+ * sequence into fresh table entries and a place for each token, with nothing
+ * read back to the host.  For sequence b with n = seq_lens[b] tokens:
+ *   new_lens[b] >= 0  so many tokens are appended: the sequence gets
+ *                     ceil((n + new) / P) - ceil(n / P) fresh pages;
+ *   new_lens[b] == -1 the sequence has ended: its ceil(n / P) pages are free
+ *                     again and its length becomes 0 (its table row is left).
+ * Freed pages are pushed onto the stack in (sequence, page) order; then the
+ * fresh pages are popped in the same order.  Table entries past a sequence's
+ * pages are left as they were.
+ *   page_table      int32 [batch][max_pages_per_seq], updated in place
+ *   seq_lens        int32 [batch];  new_lens int32 [batch]
+ *   free_pages      int32 [num_free], the stack, entries [0, free_count) valid,
+ *                   updated in place;  free_count int32 [1]
+ *   seq_lens_out    int32 [batch], may be seq_lens
+ *   free_count_out  int32 [1], may be free_count
+ *   cu_tokens       int32 [batch + 1]: first token of each sequence in the
+ *                   step, and their number
+ *   positions       int32 [max_tokens], slots int64 [max_tokens], seq_ids int32
+ *                   [max_tokens] (nullable): of token i of the step its position
+ *                   in its sequence, its slot (physical page * page_size +
+ *                   offset) and its sequence; 0, -1 and -1 past the last token.
+ * A step that cannot be taken as a whole (a length out of [0, max_pages_per_seq
+ * * page_size] before or after it, new_lens < -1, free_count out of [0,
+ * num_free]: SA_ERR_DEVICE_FAULT; more tokens than max_tokens, more pages than
+ * are free, more free pages than num_free: SA_ERR_CAPACITY) is recorded and
+ * changes nothing: lengths and free count are copied, cu_tokens is 0 and every
+ * slot -1.  A page number out of [0, num_pages) in the table or on the stack is
+ * recorded; its tokens get slot -1 (and a fresh table entry -1).
+ *   page_size in {16, 64}, batch <= 4096 (SA_ERR_UNSUPPORTED otherwise).
+ *   ws  any workspace of at least 256 bytes (only its status word is used).
+ */
+typedef struct {
+    int32_t *page_table;
+    const int32_t *seq_lens;
+    const int32_t *new_lens;
+    int32_t *free_pages;
+    const int32_t *free_count;
+    int32_t *seq_lens_out;
+    int32_t *free_count_out;
+    int32_t *cu_tokens;
+    int32_t *positions;
+    int64_t *slots;
+    int32_t *seq_ids;
+    int32_t batch;
+    int32_t page_size;
+    int32_t max_pages_per_seq;
+    int32_t num_pages;
+    int32_t num_free;
+    int32_t max_tokens;
+} sa_plan_args;
+
+SA_API sa_status sa_plan_append(const sa_plan_args *args, void *ws, size_t ws_bytes, sa_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 7. The 4-bit KV cache                                                    */
+/* ------------------------------------------------------------------------ */
+/*
+ * A paged cache as sa_kv_cache, with keys and values of one token and kv head
+ * in one record of head_dim + 16 bytes (144 instead of 512 at head_dim 128):
+ *   kv  uint8 [num_pages][num_kv_heads][page_size][head_dim + 16]
+ *       bytes [0, d/2)   key codes: channel 2j in the low nibble of byte j,
+ *                        channel 2j + 1 in the high one
+ *       bytes [d/2, d)   value codes, likewise
+ *       bytes [d, d+16)  8 bf16: {scale, zero} of key channels [0, d/2), of key
+ *                        channels [d/2, d), and of the value's two halves
+ * A code c stands for zero + scale * c.  Storing a half row x: zero = bf16(min
+ * x), scale = bf16((max x - min x) / 15), each by way of fp32, and c = (x -
+ * zero) / scale to the nearest whole number, ties to even, in [0, 15] (0 where
+ * scale is 0).  A half row with a value that is not finite, or whose scale or
+ * zero would not be, is stored with scale and zero NaN.
+ * Supported as for sa_kv_cache; also num_pages * num_kv_heads * page_size <
+ * 2^32 - 1 (SA_ERR_UNSUPPORTED otherwise).  kv is 16-byte aligned.
+ */
+typedef struct {
+    void *kv;
+    const int32_t *page_table;
+    const int32_t *seq_lens;
+    int32_t batch;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t max_pages_per_seq;
+    int32_t num_pages;
+} sa_kv4_cache;
+
+/* ------------------------------------------------------------------------ */
+/* 8. sa_rope_append -- per-head norm, rotary positions, store into the cache */
+/* ------------------------------------------------------------------------ */
+/*
+ * [DA-1] (the paged cache the masks read from holds rotated keys).  For every
+ * token t and head, over the head's head_dim channels:
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (skipped where weight is NULL)
+ *   the first rot_dim channels turned pairwise by positions[t] * inv_freq[i]:
+ *     (a, b) -> (a cos - b sin, b cos + a sin), a and b channels i and i +
+ *     rot_dim / 2, or 2i and 2i + 1 with `interleaved`
+ * for queries and keys; values are taken as they are.  Angles are formed in
+ * fp64, norms and rotations in fp32 (fp64 for keys of a 4-bit cache, whose
+ * stored codes are exactly those of the definition).  Queries go to q_out,
+ * keys and values to slot slots[t] of the cache (k and v of `kv` are written);
+ * slots[t] == -1 stores nothing and still gives the query.  The cache's page
+ * table and lengths are not read.  Two tokens must not name the same slot.
+ *   q, k, v     bf16 [num_tokens][heads][head_dim], heads contiguous, tokens
+ *               q_stride / k_stride / v_stride elements apart (multiples of 8),
+ *               16-byte aligned: for instance the parts of one packed projection
+ *   positions   int32 [num_tokens];  slots int64 [num_tokens]
+ *   inv_freq    fp32 [rot_dim / 2] (NULL when rot_dim is 0); rot_dim a multiple
+ *               of 16 in [0, head_dim]
+ *   q_weight, k_weight  [head_dim] of weight_dtype, 16-byte aligned, nullable
+ *   q_out       bf16 [num_tokens][num_q_heads][head_dim], q_out_stride; may be q
+ *               itself (same stride), otherwise must not overlap the inputs
+ * A slot out of [-1, num_pages * page_size) stores nothing and is recorded.
+ * The cache's head_dim in {64, 128}, page_size in {16, 64}; num_q_heads need
+ * not be a multiple of num_kv_heads; kv->batch may be 0.
+ *   ws  any workspace of at least 256 bytes (only its status word is used).
+ */
+typedef struct {
+    const void *q;
+    const void *k;
+    const void *v;
+    int64_t q_stride;
+    int64_t k_stride;
+    int64_t v_stride;
+    void *q_out;
+    int64_t q_out_stride;
+    const int32_t *positions;
+    const int64_t *slots;
+    const float *inv_freq;
+    const void *q_weight;
+    const void *k_weight;
+    sa_dtype weight_dtype;
+    float eps;
+    int32_t num_tokens;
+    int32_t num_q_heads;
+    int32_t rot_dim;
+    int32_t interleaved;
+} sa_append_args;
+
+SA_API sa_status sa_rope_append(const sa_kv_cache *kv, const sa_append_args *args, void *ws, size_t ws_bytes,
+                                sa_stream_t stream);
+SA_API sa_status sa_rope_append_kv4(const sa_kv4_cache *kv, const sa_append_args *args, void *ws, size_t ws_bytes,
+                                    sa_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 9. sa_expand_kv4 -- pages of a 4-bit cache as bf16 pages                 */
+/* ------------------------------------------------------------------------ */
+/*
+ * [RBS] "关键技术点" 2: the selections and the prefill read bf16 pages; this
+ * makes them from a 4-bit cache.  For i < n, page i of k_out and v_out (bf16
+ * [n][num_kv_heads][page_size][head_dim]) receives zero + scale * code of page
+ * pages[i] (int32 [n], device), rounded to bf16.  pages[i] == -1 leaves page i
+ * as it was; other numbers out of [0, num_pages) too, and are recorded.
+ *   ws  any workspace of at least 256 bytes (only its status word is used).
+ */
+SA_API sa_status sa_expand_kv4(const sa_kv4_cache *kv, const int32_t *pages, int32_t n, void *k_out, void *v_out,
+                               void *ws, size_t ws_bytes, sa_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 10. sa_sparse_decode_attn_kv4 -- decode over a 4-bit cache               */
+/* ------------------------------------------------------------------------ */
+/*
+ * What sa_sparse_decode_attn computes, over the values a 4-bit cache stands
+ * for: same selections, outputs and errors.  Scores are accumulated in fp32 (an
+ * fp32 query as bf16 high + low parts); a softmax weight times its row's scale
+ * enters the P.V product as bf16.
+ *   num_splits in [0, 64]; 0 lets the library choose from the sizes.
+ *   ws  workspace of sa_kv4_decode_workspace_bytes(...) bytes
+ */
+SA_API sa_status sa_sparse_decode_attn_kv4(const sa_kv4_cache *kv, const void *q, sa_dtype q_dtype,
+                                           int32_t num_q_heads, const sa_selection *sel, float scale,
+                                           int32_t num_splits, void *out, float *lse_out, void *ws,
+                                           size_t ws_bytes, sa_stream_t stream);
+
+/* Bytes of workspace the call above needs (a multiple of 256), enough for any
+ * selection with num_splits 0; 0 when the description is invalid.  Host only. */
+SA_API size_t sa_kv4_decode_workspace_bytes(const sa_kv4_cache *kv, int32_t num_q_heads, int32_t num_splits);
 
 /* ------------------------------------------------------------------------ */
 /* Workspace sizing, status                                                 */

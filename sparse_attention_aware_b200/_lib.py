@@ -24,13 +24,35 @@ OP_SELECT_TOPK, OP_SELECT_BLOCKS, OP_DECODE, OP_PREFILL = 1, 2, 3, 4
 EXPORTS = ("sa_select_topk", "sa_select_blocks", "sa_sparse_decode_attn", "sa_sparse_prefill_attn",
            "sa_workspace_bytes", "sa_workspace_init", "sa_read_device_status", "sa_status_string",
            "sa_version", "sa_sparse_decode_attn_noalloc", "sa_fetch_pages", "sa_tier_plan",
-           "sa_tier_plan_scratch_ints", "sa_check_bounded_wait")
+           "sa_tier_plan_scratch_ints", "sa_check_bounded_wait", "sa_plan_append", "sa_rope_append",
+           "sa_rope_append_kv4", "sa_expand_kv4", "sa_sparse_decode_attn_kv4", "sa_kv4_decode_workspace_bytes")
 
 
 class KVCacheS(ctypes.Structure):
     _fields_ = [("k", c_vp), ("v", c_vp), ("page_table", c_vp), ("seq_lens", c_vp),
                 ("batch", c_i32), ("num_kv_heads", c_i32), ("head_dim", c_i32),
                 ("page_size", c_i32), ("max_pages_per_seq", c_i32), ("num_pages", c_i32)]
+
+
+class KV4CacheS(ctypes.Structure):
+    _fields_ = [("kv", c_vp), ("page_table", c_vp), ("seq_lens", c_vp),
+                ("batch", c_i32), ("num_kv_heads", c_i32), ("head_dim", c_i32),
+                ("page_size", c_i32), ("max_pages_per_seq", c_i32), ("num_pages", c_i32)]
+
+
+class PlanArgsS(ctypes.Structure):
+    _fields_ = [("page_table", c_vp), ("seq_lens", c_vp), ("new_lens", c_vp), ("free_pages", c_vp),
+                ("free_count", c_vp), ("seq_lens_out", c_vp), ("free_count_out", c_vp), ("cu_tokens", c_vp),
+                ("positions", c_vp), ("slots", c_vp), ("seq_ids", c_vp), ("batch", c_i32), ("page_size", c_i32),
+                ("max_pages_per_seq", c_i32), ("num_pages", c_i32), ("num_free", c_i32), ("max_tokens", c_i32)]
+
+
+class AppendArgsS(ctypes.Structure):
+    _fields_ = [("q", c_vp), ("k", c_vp), ("v", c_vp), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_out", c_vp), ("q_out_stride", ctypes.c_int64),
+                ("positions", c_vp), ("slots", c_vp), ("inv_freq", c_vp), ("q_weight", c_vp), ("k_weight", c_vp),
+                ("weight_dtype", c_i32), ("eps", c_f32), ("num_tokens", c_i32), ("num_q_heads", c_i32),
+                ("rot_dim", c_i32), ("interleaved", c_i32)]
 
 
 class SelectionS(ctypes.Structure):
@@ -82,6 +104,14 @@ def load(path: str = LIB_PATH):
                                          c_vp, c_vp, c_vp, c_size, c_vp]
     L.sa_tier_plan.argtypes = [c_vp, ctypes.c_int64, c_vp, c_vp, c_i32, ctypes.c_int64, c_vp, c_i32, c_vp, c_i32,
                                c_vp, c_vp, c_vp, c_vp, ctypes.c_int64]
+    L.sa_plan_append.argtypes = [P(PlanArgsS), c_vp, c_size, c_vp]
+    L.sa_rope_append.argtypes = [P(KVCacheS), P(AppendArgsS), c_vp, c_size, c_vp]
+    L.sa_rope_append_kv4.argtypes = [P(KV4CacheS), P(AppendArgsS), c_vp, c_size, c_vp]
+    L.sa_expand_kv4.argtypes = [P(KV4CacheS), c_vp, c_i32, c_vp, c_vp, c_vp, c_size, c_vp]
+    L.sa_sparse_decode_attn_kv4.argtypes = [P(KV4CacheS), c_vp, c_i32, c_i32, P(SelectionS), c_f32, c_i32,
+                                            c_vp, c_vp, c_vp, c_size, c_vp]
+    L.sa_kv4_decode_workspace_bytes.argtypes = [P(KV4CacheS), c_i32, c_i32]
+    L.sa_kv4_decode_workspace_bytes.restype = c_size
     L.sa_check_bounded_wait.argtypes = [ctypes.c_int64, c_vp, c_size, c_vp]
     L.sa_tier_plan_scratch_ints.argtypes = [ctypes.c_int64, c_i32]
     L.sa_tier_plan_scratch_ints.restype = ctypes.c_int64
@@ -94,7 +124,8 @@ def load(path: str = LIB_PATH):
     L.sa_version.restype = c_i32
     for fn in ("sa_select_topk", "sa_select_blocks", "sa_sparse_decode_attn", "sa_sparse_prefill_attn",
                "sa_workspace_init", "sa_read_device_status", "sa_sparse_decode_attn_noalloc", "sa_fetch_pages",
-               "sa_tier_plan", "sa_check_bounded_wait"):
+               "sa_tier_plan", "sa_check_bounded_wait", "sa_plan_append", "sa_rope_append", "sa_rope_append_kv4",
+               "sa_expand_kv4", "sa_sparse_decode_attn_kv4"):
         getattr(L, fn).restype = c_i32
     _lib = L
     return L

@@ -10,12 +10,14 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import functools
+import inspect
 import math
 from typing import Optional, Sequence
 
 import torch
 
 from . import _lib as L
+from .cache import PagedCache4, PagePool
 
 
 class SAError(RuntimeError):
@@ -82,6 +84,33 @@ def kv_struct(cache, device=None) -> L.KVCacheS:
                          % sorted(str(d) for d in devs))
     return L.KVCacheS(k.data_ptr(), v.data_ptr(), pt.data_ptr(), sl.data_ptr(), pt.shape[0], k.shape[1],
                       k.shape[3], k.shape[2], pt.shape[1], k.shape[0])
+
+
+def kv4_struct(cache: PagedCache4, device=None) -> L.KV4CacheS:
+    """``kv_struct`` for a 4-bit cache."""
+    kv, pt, sl = cache.kv, cache.page_table, cache.seq_lens
+    if kv.dtype != torch.uint8 or kv.dim() != 4 or not kv.is_contiguous() or kv.shape[3] <= 16:
+        raise ValueError("4-bit KV cache: kv must be a contiguous uint8 [num_pages][Hkv][P][d + 16] tensor")
+    if pt.dtype != torch.int32 or pt.dim() != 2 or not pt.is_contiguous():
+        raise ValueError("4-bit KV cache: page_table must be a contiguous int32 [B][max_pages] tensor")
+    if sl.dtype != torch.int32 or sl.dim() != 1 or sl.shape[0] != pt.shape[0] or not sl.is_contiguous():
+        raise ValueError("4-bit KV cache: seq_lens must be a contiguous int32 [B] tensor, B = %d" % pt.shape[0])
+    dev = kv.device
+    if pt.device != dev or sl.device != dev or (device is not None and dev != torch.device(device)):
+        raise ValueError("4-bit KV cache: kv, page_table, seq_lens and the queries must be on one device, got %s"
+                         % sorted({str(t.device) for t in (kv, pt, sl)} | {str(device)}))
+    n, h, p, r = kv.shape
+    return L.KV4CacheS(kv.data_ptr(), pt.data_ptr(), sl.data_ptr(), pt.shape[0], h, r - 16, p, pt.shape[1], n)
+
+
+def _geometry(cache, device=None) -> L.KVCacheS:
+    """``kv_struct``, where a 4-bit cache is its lengths and page geometry (all
+    that the span selection reads)."""
+    if not isinstance(cache, PagedCache4):
+        return kv_struct(cache, device)
+    c = kv4_struct(cache, device)
+    return L.KVCacheS(None, None, c.page_table, c.seq_lens, c.batch, c.num_kv_heads, c.head_dim, c.page_size,
+                      c.max_pages_per_seq, c.num_pages)
 
 
 class Workspace:
@@ -158,7 +187,7 @@ def _ws(ws: Optional[Workspace], device, stream=None) -> Workspace:
 
 def workspace_bytes(op: int, cache, num_q_heads=0, k=0, num_splits=0, num_tokens=0,
                     block_args: Optional[L.BlockSelectArgsS] = None) -> int:
-    kv = kv_struct(cache)
+    kv = _geometry(cache)
     q = L.WsQueryS(num_q_heads, k, num_splits, num_tokens,
                    ctypes.pointer(block_args) if block_args is not None else None)
     n = L.load().sa_workspace_bytes(op, ctypes.byref(kv), ctypes.byref(q))
@@ -187,6 +216,31 @@ def _qdtype(q: torch.Tensor) -> int:
     if q.dtype == torch.bfloat16:
         return L.DTYPE_BF16
     raise TypeError("q must be fp32 or bf16")
+
+
+def _on_call_device(fn):
+    """``_on_call_stream``, and the call's kernels go to the device of the
+    call's first tensor also where that is not the current one."""
+    first = next(iter(inspect.signature(fn).parameters))
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        s = kw.get("stream")
+        if s is not None:
+            with torch.cuda.stream(s):
+                return fn(*args, **kw)
+        dev = _device_of(args[0] if args else kw[first])
+        if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+            return fn(*args, **kw)
+        with torch.cuda.device(dev):
+            return fn(*args, **kw)
+    return call
+
+
+def _device_of(x) -> torch.device:
+    if isinstance(x, torch.Tensor):
+        return x.device
+    return x.kv.device if isinstance(x, PagedCache4) else x.k.device
 
 
 # --------------------------------------------------------------------------
@@ -269,7 +323,11 @@ def select_topk(cache, q: torch.Tensor, k: int, idx: Optional[torch.Tensor] = No
 def sparse_decode_attn(cache, q: torch.Tensor, sel, scale: Optional[float] = None, num_splits: int = 1,
                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                        want_lse: bool = True, ws: Optional[Workspace] = None, stream=None):
-    """Split-KV sparse decode + combine (``sa_sparse_decode_attn``).  Returns (out bf16, lse fp32)."""
+    """Split-KV sparse decode + combine (``sa_sparse_decode_attn``, or
+    ``sa_sparse_decode_attn_kv4`` over a PagedCache4, where ``num_splits=0``
+    lets the library choose).  Returns (out bf16, lse fp32)."""
+    if isinstance(cache, PagedCache4):
+        return _decode_kv4(cache, q, sel, scale, num_splits, out, lse, want_lse, ws, stream)
     B, Hq, d = q.shape
     dev = q.device
     scale = 1.0 / math.sqrt(d) if scale is None else scale
@@ -289,6 +347,197 @@ def sparse_decode_attn(cache, q: torch.Tensor, sel, scale: Optional[float] = Non
                                           ctypes.byref(s), scale, num_splits, _ptr(out), _ptr(lse), wp, wn,
                                           _stream(stream)), "sa_sparse_decode_attn")
     return out, lse
+
+
+@_on_call_device
+def _decode_kv4(cache: PagedCache4, q, sel, scale, num_splits, out, lse, want_lse, ws, stream):
+    B, Hq, d = q.shape
+    dev = q.device
+    kv = kv4_struct(cache, dev)
+    if (B, d) != (kv.batch, kv.head_dim):
+        raise ValueError("sparse_decode_attn: q is [%d][%d][%d], the 4-bit cache has batch %d and head_dim %d"
+                         % (B, Hq, d, kv.batch, kv.head_dim))
+    q = q.contiguous()
+    if out is None:
+        out = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, (B, Hq, d), torch.bfloat16, dev, "sparse_decode_attn out")
+    if lse is not None:
+        _need(lse, (B, Hq), torch.float32, dev, "sparse_decode_attn lse")
+    elif want_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    _check_selection(sel, B, Hq, dev)
+    s = sel.struct()
+    lib = L.load()
+    need = lib.sa_kv4_decode_workspace_bytes(ctypes.byref(kv), Hq, num_splits)
+    wp, wn = _ws(ws, dev, stream).aligned(need, stream)
+    _check(lib.sa_sparse_decode_attn_kv4(ctypes.byref(kv), q.data_ptr(), _qdtype(q), Hq, ctypes.byref(s),
+                                         1.0 / math.sqrt(d) if scale is None else scale, num_splits, out.data_ptr(),
+                                         _ptr(lse), wp, wn, _stream(stream)), "sa_sparse_decode_attn_kv4")
+    return out, lse
+
+
+# --------------------------------------------------------------------------
+# a step's pages, keys and values
+# --------------------------------------------------------------------------
+@dataclasses.dataclass
+class AppendPlan:
+    """Where a step's tokens go (``plan_append``)."""
+    cu_tokens: torch.Tensor   # int32 [B + 1] first token of each sequence, and their number
+    positions: torch.Tensor   # int32 [max_tokens] position in the sequence (0 past the last token)
+    slots: torch.Tensor       # int64 [max_tokens] page * P + offset (-1 past the last token)
+    seq_ids: torch.Tensor     # int32 [max_tokens] sequence (-1 past the last token)
+
+    @staticmethod
+    def empty(batch: int, max_tokens: int, device) -> "AppendPlan":
+        return AppendPlan(torch.empty(batch + 1, dtype=torch.int32, device=device),
+                          torch.empty(max_tokens, dtype=torch.int32, device=device),
+                          torch.empty(max_tokens, dtype=torch.int64, device=device),
+                          torch.empty(max_tokens, dtype=torch.int32, device=device))
+
+
+@_on_call_device
+def plan_append(page_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torch.Tensor, pool: PagePool,
+                max_tokens: int, seq_lens_out: Optional[torch.Tensor] = None,
+                free_count_out: Optional[torch.Tensor] = None, plan: Optional[AppendPlan] = None,
+                ws: Optional[Workspace] = None, stream=None) -> AppendPlan:
+    """Pages, positions and slots of a step from the sequences' lengths
+    (``sa_plan_append``): ``new_lens[b]`` tokens are appended to sequence b (-1:
+    it has ended).  The page table and the pool's stack are updated in place,
+    and so are ``seq_lens`` and ``pool.free_count`` unless ``seq_lens_out`` /
+    ``free_count_out`` take the new values.  A step that does not fit changes
+    nothing, gives every token slot -1 and is recorded in the workspace."""
+    dev = page_table.device
+    if page_table.dim() != 2:
+        raise ValueError("plan_append: page_table must be int32 [B][max_pages]")
+    B, mp = page_table.shape
+    _need(page_table, (B, mp), torch.int32, dev, "plan_append page_table")
+    _need(seq_lens, (B,), torch.int32, dev, "plan_append seq_lens")
+    _need(new_lens, (B,), torch.int32, dev, "plan_append new_lens")
+    _need(pool.free_pages, (pool.free_pages.numel(),), torch.int32, dev, "plan_append pool.free_pages")
+    _need(pool.free_count, (1,), torch.int32, dev, "plan_append pool.free_count")
+    if seq_lens_out is None:
+        seq_lens_out = seq_lens
+    else:
+        _need(seq_lens_out, (B,), torch.int32, dev, "plan_append seq_lens_out")
+    if free_count_out is None:
+        free_count_out = pool.free_count
+    else:
+        _need(free_count_out, (1,), torch.int32, dev, "plan_append free_count_out")
+    if plan is None:
+        plan = AppendPlan.empty(B, max_tokens, dev)
+    else:
+        _need(plan.cu_tokens, (B + 1,), torch.int32, dev, "plan_append plan.cu_tokens")
+        _need(plan.positions, (max_tokens,), torch.int32, dev, "plan_append plan.positions")
+        _need(plan.slots, (max_tokens,), torch.int64, dev, "plan_append plan.slots")
+        _need(plan.seq_ids, (max_tokens,), torch.int32, dev, "plan_append plan.seq_ids")
+    a = L.PlanArgsS(page_table.data_ptr(), seq_lens.data_ptr(), new_lens.data_ptr(), pool.free_pages.data_ptr(),
+                    pool.free_count.data_ptr(), seq_lens_out.data_ptr(), free_count_out.data_ptr(),
+                    plan.cu_tokens.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr(),
+                    plan.seq_ids.data_ptr(), B, pool.page_size, mp, pool.num_pages, pool.free_pages.numel(),
+                    max_tokens)
+    wp, wn = _ws(ws, dev, stream).aligned(256, stream)
+    _check(L.load().sa_plan_append(ctypes.byref(a), wp, wn, _stream(stream)), "sa_plan_append")
+    return plan
+
+
+def _rows(x: torch.Tensor, what: str, shape, device):
+    """``x`` as the library reads it -- bf16 [T][H][d] with heads contiguous and
+    tokens a multiple of 8 elements apart, 16-byte aligned (parts of a packed
+    projection are taken as they are; other layouts are copied) -- and the
+    elements between its tokens."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError("rope_append: %s must be bf16, got %s" % (what, x.dtype))
+    if tuple(x.shape) != shape or x.device != device:
+        raise ValueError("rope_append: %s must be %s on %s, got %s on %s"
+                         % (what, shape, device, tuple(x.shape), x.device))
+    st, sh, sd = x.stride()
+    if sd != 1 or (sh != shape[2] and shape[1] > 1) or (st % 8 and shape[0] > 1) or x.data_ptr() % 16:
+        x = x.contiguous()
+        st = shape[1] * shape[2]
+    return x, (st if shape[0] > 1 else shape[1] * shape[2])
+
+
+@_on_call_device
+def rope_append(cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                slots: torch.Tensor, inv_freq: Optional[torch.Tensor] = None,
+                q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                eps: float = 1e-6, interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                ws: Optional[Workspace] = None, stream=None) -> torch.Tensor:
+    """Per-head RMS norm (where a weight is given) and rotary positions of a
+    step's queries and keys, and the store of keys and values into ``cache``, a
+    PagedCache or a PagedCache4 (``sa_rope_append``, ``sa_rope_append_kv4``).
+    q [T][Hq][d], k and v [T][Hkv][d] bf16; positions int32 [T]; slots int64 [T]
+    (-1: not stored); inv_freq fp32 [rot_dim / 2], None for no rotation.  Returns
+    the queries, bf16 [T][Hq][d] (in ``q_out`` if given, which may be ``q``)."""
+    four = isinstance(cache, PagedCache4)
+    dev = q.device
+    if q.dim() != 3:
+        raise ValueError("rope_append: q must be bf16 [T][Hq][d], got shape %s" % (tuple(q.shape),))
+    T, Hq, d = q.shape
+    kv = kv4_struct(cache, dev) if four else kv_struct(cache, dev)
+    if d != kv.head_dim:
+        raise ValueError("rope_append: head_dim %d, the cache's is %d" % (d, kv.head_dim))
+    if q_out is not None and q_out is not q:
+        if q_out.dtype != torch.bfloat16 or tuple(q_out.shape) != (T, Hq, d) or q_out.device != dev or                 q_out.stride(2) != 1 or q_out.stride(1) != d or q_out.stride(0) % 8 or q_out.data_ptr() % 16:
+            raise ValueError("rope_append q_out: need a bf16 [T][Hq][d] tensor on %s with contiguous heads" % dev)
+    src, qs = _rows(q, "q", (T, Hq, d), dev)
+    if q_out is q and src is not q:
+        raise ValueError("rope_append q_out: q is not laid out for an update in place")
+    k, ks = _rows(k, "k", (T, kv.num_kv_heads, d), dev)
+    v, vs = _rows(v, "v", (T, kv.num_kv_heads, d), dev)
+    _need(positions, (T,), torch.int32, dev, "rope_append positions")
+    _need(slots, (T,), torch.int64, dev, "rope_append slots")
+    rot = 0
+    if inv_freq is not None:
+        _need(inv_freq, (inv_freq.numel(),), torch.float32, dev, "rope_append inv_freq")
+        rot = 2 * inv_freq.numel()
+    wt = torch.bfloat16
+    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            wt = w.dtype
+            if wt not in (torch.bfloat16, torch.float32):
+                raise TypeError("rope_append: %s must be bf16 or fp32, got %s" % (what, wt))
+            _need(w, (d,), wt, dev, "rope_append " + what)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise TypeError("rope_append: q_weight and k_weight must be of one type")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+    a = L.AppendArgsS(src.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, q_out.data_ptr(),
+                      q_out.stride(0) if T > 1 else Hq * d, positions.data_ptr(), slots.data_ptr(),
+                      None if rot == 0 else inv_freq.data_ptr(), None if q_weight is None else q_weight.data_ptr(),
+                      None if k_weight is None else k_weight.data_ptr(), L.DTYPE_F32 if wt == torch.float32 else
+                      L.DTYPE_BF16, eps, T, Hq, rot, int(interleaved))
+    wp, wn = _ws(ws, dev, stream).aligned(256, stream)
+    lib = L.load()
+    fn = lib.sa_rope_append_kv4 if four else lib.sa_rope_append
+    _check(fn(ctypes.byref(kv), ctypes.byref(a), wp, wn, _stream(stream)),
+           "sa_rope_append_kv4" if four else "sa_rope_append")
+    return q_out
+
+
+@_on_call_device
+def expand_kv4(cache: PagedCache4, pages: torch.Tensor, k: Optional[torch.Tensor] = None,
+               v: Optional[torch.Tensor] = None, ws: Optional[Workspace] = None, stream=None):
+    """Pages of a 4-bit cache as bf16 pages (``sa_expand_kv4``): ``pages`` int32
+    [n] (-1: that output page is left as it was) -> (k, v) bf16 [n][Hkv][P][d],
+    pools that a PagedCache can hold."""
+    dev = cache.kv.device
+    kv = kv4_struct(cache)
+    shape = (pages.numel(), kv.num_kv_heads, kv.page_size, kv.head_dim)
+    _need(pages, (pages.numel(),), torch.int32, dev, "expand_kv4 pages")
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(k, shape, torch.bfloat16, dev, "expand_kv4 k")
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(v, shape, torch.bfloat16, dev, "expand_kv4 v")
+    wp, wn = _ws(ws, dev, stream).aligned(256, stream)
+    _check(L.load().sa_expand_kv4(ctypes.byref(kv), pages.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(), wp, wn,
+                                  _stream(stream)), "sa_expand_kv4")
+    return k, v
 
 
 @_on_call_stream
@@ -345,7 +594,7 @@ def select_blocks_spans(cache, spans: torch.Tensor, span_counts: torch.Tensor, s
     if span_round.dtype == torch.bool:
         span_round = span_round.to(torch.uint8)
     _need(span_round, (B, S), torch.uint8, dev, "select_blocks_spans span_round")
-    kv = kv_struct(cache, dev)
+    kv = _geometry(cache, dev)
     a = L.BlockSelectArgsS()
     a.mode = L.SEL_SPANS
     a.spans, a.span_counts, a.span_round = spans.data_ptr(), span_counts.data_ptr(), span_round.data_ptr()

@@ -1,0 +1,225 @@
+// Pages, positions and slots of a step, built on the device from the
+// sequences' lengths.
+//
+// Paged caches keep a sequence's tokens in fixed-size pages named by a table
+// ("语言模型能自己决定该看哪里吗？", DA state machine section: vLLM's KV
+// blocks).  For sequence b holding n_b tokens that gets a_b more (a_b = -1:
+// it has ended):
+//   held_b = ceil(n_b / P),  need_b = ceil((n_b + a_b) / P) - held_b
+// The pages of ended sequences go onto a stack of free pages in (sequence,
+// page) order, then the i-th page needed, counted in the same order, is the
+// i-th from the top.  Token i of the step belongs to the sequence b with
+// cu_b <= i < cu_{b+1} (cu: prefix sums of a), has position n_b + i - cu_b and
+// goes to slot page * P + position % P.
+//
+// One cluster: every CTA computes the prefix sums of all sequences for itself
+// (a few KB of lengths), they push the freed pages, meet at one cluster
+// barrier -- behind which the inputs may be overwritten, so lengths and the
+// free count can be updated in place -- and then share the writing of tables
+// and tokens.  Bound by latency: the dependent trips lengths -> scan -> stack
+// -> table, about 16 bytes per token beside them.
+#include <cooperative_groups.h>
+
+#include "sa_internal.h"
+
+namespace sa {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanItems = kPlanMaxBatch / kPlanThreads;   // sequences per thread
+
+struct Sums {
+    long long tok, need, back;
+};
+
+__device__ __forceinline__ Sums plus(const Sums &x, const Sums &y)
+{
+    return {x.tok + y.tok, x.need + y.need, x.back + y.back};
+}
+
+// exclusive prefix over the block; `total` receives the block's sum
+__device__ __forceinline__ Sums block_scan(Sums v, Sums *warp_sum, Sums &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sums inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sums y = {__shfl_up_sync(~0u, inc.tok, o), __shfl_up_sync(~0u, inc.need, o),
+                        __shfl_up_sync(~0u, inc.back, o)};
+        if (lane >= o) inc = plus(inc, y);
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        Sums w = warp_sum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Sums y = {__shfl_up_sync(~0u, w.tok, o), __shfl_up_sync(~0u, w.need, o),
+                            __shfl_up_sync(~0u, w.back, o)};
+            if (lane >= o) w = plus(w, y);
+        }
+        warp_sum[lane] = w;
+    }
+    __syncthreads();
+    total = warp_sum[31];
+    Sums r = {inc.tok - v.tok, inc.need - v.need, inc.back - v.back};
+    if (warp > 0) r = plus(r, warp_sum[warp - 1]);
+    return r;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
+{
+    pdl_wait();
+    pdl_trigger();
+    namespace cg = cooperative_groups;
+    extern __shared__ int plan_sm[];
+    __shared__ Sums warp_sum[32];
+    const int B = a.B, P = 1 << a.Plog2, tid = threadIdx.x;
+    int *s_old = plan_sm;            // [B] tokens held
+    int *s_new = s_old + B;          // [B] tokens to come, -1 = ended
+    int *s_need = s_new + B;         // [B] fresh pages of earlier sequences
+    int *s_cu = s_need + B;          // [B + 1]
+    const int rank = (int)cg::this_cluster().block_rank(), ranks = (int)cg::this_cluster().num_blocks();
+    const long long Lcap = (long long)a.max_pages << a.Plog2;
+
+    // ---- lengths, and what they ask for
+    Sums mine = {0, 0, 0};
+    Sums part[kPlanItems];
+    int bad = 0;
+#pragma unroll
+    for (int u = 0; u < kPlanItems; ++u) {
+        const int b = tid * kPlanItems + u;
+        part[u] = mine;
+        if (b >= B) continue;
+        int old = a.sl[b], add = a.add[b];
+        if (old < 0 || old > Lcap || add < -1 || (long long)old + add > Lcap) {
+            if (rank == 0) fault(a.st, CHK_SEQ_LEN, old < 0 || old > Lcap ? old : add);
+            bad = 1;
+        }
+        const long long held = ((long long)old + P - 1) >> a.Plog2;
+        const long long then = ((long long)old + add + P - 1) >> a.Plog2;
+        if (add < 0) mine.back += held;
+        else mine.tok += add, mine.need += then - held;
+        s_old[b] = old;
+        s_new[b] = add;
+    }
+    bad = __syncthreads_or(bad);
+    Sums all;
+    const Sums before = block_scan(mine, warp_sum, all);
+    const int count = *a.count;
+    if (count < 0 || count > a.num_free) {
+        if (rank == 0 && tid == 0) fault(a.st, CHK_COUNT, count);
+        bad = 1;
+    }
+    if (!bad) {
+        int chk = 0;
+        long long what = 0;
+        if (all.tok > a.max_tokens) chk = CHK_CAPACITY_TOKENS, what = all.tok;
+        else if (count + all.back > a.num_free) chk = CHK_CAPACITY_PAGES, what = count + all.back;
+        else if (all.need > count + all.back) chk = CHK_CAPACITY_PAGES, what = all.need;
+        if (chk) {
+            if (rank == 0 && tid == 0)
+                record(a.st, SA_ERR_CAPACITY, chk, (int)(what > 0x7fffffff ? 0x7fffffff : what));
+            bad = 1;
+        }
+    }
+    // a step that cannot be taken changes nothing
+    if (bad) all = {0, 0, 0};
+    const int top = count + (int)all.back;
+#pragma unroll
+    for (int u = 0; u < kPlanItems; ++u) {
+        const int b = tid * kPlanItems + u;
+        if (b >= B) continue;
+        const Sums x = plus(before, part[u]);
+        s_cu[b] = bad ? 0 : (int)x.tok;
+        s_need[b] = (int)x.need;
+        // pages of an ended sequence onto the stack (few sequences end in a step)
+        if (!bad && s_new[b] < 0) {
+            const int held = (s_old[b] + P - 1) >> a.Plog2;
+            for (int p = rank; p < held; p += ranks) {
+                const int page = a.table[(size_t)b * a.max_pages + p];
+                if (page < 0 || page >= a.num_pages) fault(a.st, CHK_PAGE, page);
+                a.free[count + x.back + p] = page;
+            }
+        }
+    }
+    if (tid == 0) s_cu[B] = (int)all.tok;
+    cg::this_cluster().sync();   // every CTA has read the inputs; the stack is whole
+
+    // ---- lengths, prefix sums, fresh table entries
+    const int gtid = rank * kPlanThreads + tid, threads = ranks * kPlanThreads;
+    for (int b = gtid; b < B; b += threads) {
+        const int add = s_new[b];
+        a.sl_out[b] = bad ? s_old[b] : add < 0 ? 0 : s_old[b] + add;
+        a.cu[b] = s_cu[b];
+    }
+    if (gtid == 0) {
+        a.cu[B] = (int)all.tok;
+        *a.count_out = bad ? count : top - (int)all.need;
+    }
+    if (!bad) {
+        for (int b = gtid >> 5; b < B; b += threads >> 5) {
+            const int old = s_old[b], add = s_new[b];
+            if (add <= 0) continue;
+            const int held = (old + P - 1) >> a.Plog2, then = (old + add + P - 1) >> a.Plog2;
+            for (int p = held + (gtid & 31); p < then; p += 32) {
+                int page = a.free[top - 1 - (s_need[b] + p - held)];
+                if (page < 0 || page >= a.num_pages) {
+                    fault(a.st, CHK_PAGE, page);
+                    page = -1;
+                }
+                a.table[(size_t)b * a.max_pages + p] = page;
+            }
+        }
+    }
+    // ---- tokens
+    const int total = (int)all.tok;
+    for (int i = gtid; i < a.max_tokens; i += threads) {
+        int pos = 0, seq = -1;
+        long long slot = -1;
+        if (i < total) {
+            int lo = 0, hi = B - 1;   // the last b with cu_b <= i holds i (empty ones before it have the same cu)
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (s_cu[mid] <= i) lo = mid; else hi = mid - 1;
+            }
+            seq = lo;
+            pos = s_old[seq] + i - s_cu[seq];
+            const int held = (s_old[seq] + P - 1) >> a.Plog2, p = pos >> a.Plog2;
+            const int page = p < held ? a.table[(size_t)seq * a.max_pages + p]
+                                      : a.free[top - 1 - (s_need[seq] + p - held)];
+            if (page < 0 || page >= a.num_pages) fault(a.st, CHK_PAGE, page);
+            else slot = ((long long)page << a.Plog2) + (pos & (P - 1));
+        }
+        a.pos[i] = pos;
+        a.slots[i] = slot;
+        if (a.seq_ids) a.seq_ids[i] = seq;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_plan(const PlanArgs &a, cudaStream_t s)
+{
+    const size_t smem = (size_t)(4 * a.B + 1) * sizeof(int);
+    cudaError_t e = cudaFuncSetAttribute(k_plan_append, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (4 * kPlanMaxBatch + 1) * (int)sizeof(int));
+    if (e != cudaSuccess) return e;
+    const int ctas = a.max_tokens > 4 * kPlanThreads || a.B > kPlanThreads ? 8 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_plan_append, a);
+}
+
+}  // namespace sa

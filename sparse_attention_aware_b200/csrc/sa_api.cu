@@ -38,7 +38,8 @@ inline int ilog2(int x)
 }
 
 // Validate the cache descriptor (host-visible fields and pointers).
-sa_status check_cache(const sa_kv_cache *kv, CacheArgs *c)
+// pools = false: the call reads neither k nor v, which may then be null.
+sa_status check_cache(const sa_kv_cache *kv, CacheArgs *c, bool pools = true)
 {
     if (!kv) return SA_ERR_INVALID_ARGUMENT;
     if (kv->batch < 0 || kv->num_kv_heads <= 0 || kv->head_dim <= 0 || kv->page_size <= 0 ||
@@ -48,7 +49,7 @@ sa_status check_cache(const sa_kv_cache *kv, CacheArgs *c)
     if (kv->page_size != 16 && kv->page_size != 64) return SA_ERR_UNSUPPORTED;
     if ((long long)kv->max_pages_per_seq * kv->page_size > (1LL << 30)) return SA_ERR_UNSUPPORTED;
     if (kv->batch > 0) {
-        if (!kv->k || !kv->v || !kv->page_table || !kv->seq_lens) return SA_ERR_INVALID_ARGUMENT;
+        if ((pools && (!kv->k || !kv->v)) || !kv->page_table || !kv->seq_lens) return SA_ERR_INVALID_ARGUMENT;
         if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->page_table, 4) ||
             !aligned(kv->seq_lens, 4))
             return SA_ERR_INVALID_ARGUMENT;
@@ -66,6 +67,58 @@ sa_status check_cache(const sa_kv_cache *kv, CacheArgs *c)
         c->max_pages = kv->max_pages_per_seq;
         c->num_pages = kv->num_pages;
     }
+    return SA_OK;
+}
+
+// A 4-bit cache, as the CacheArgs whose k is the records' pool.
+sa_status check_cache4(const sa_kv4_cache *kv, CacheArgs *c)
+{
+    if (!kv) return SA_ERR_INVALID_ARGUMENT;
+    const sa_kv_cache as = {kv->kv, kv->kv, kv->page_table, kv->seq_lens, kv->batch, kv->num_kv_heads,
+                            kv->head_dim, kv->page_size, kv->max_pages_per_seq, kv->num_pages};
+    sa_status st = check_cache(&as, c);
+    if (st != SA_OK) return st;
+    // the kernels number records with 32 bits, all ones meaning none
+    if ((unsigned long long)kv->num_pages * kv->num_kv_heads * kv->page_size >= 0xffffffffull)
+        return SA_ERR_UNSUPPORTED;
+    return SA_OK;
+}
+
+// CTAs per (sequence, split) of a block-list decode over a 4-bit cache
+int kv4_group_rows(const sa_kv4_cache *kv, int Hq) { return kv->num_kv_heads * ((Hq / kv->num_kv_heads + 15) / 16); }
+
+// Fields of a decode that both cache kinds share, checked and set.
+sa_status check_decode(int B, int Hkv, const void *q, sa_dtype q_dtype, int Hq, const sa_selection *sel, float scale,
+                       const void *out, const float *lse, DecodeArgs *a)
+{
+    if (Hq <= 0 || !sel) return SA_ERR_INVALID_ARGUMENT;
+    if (q_dtype != SA_DTYPE_F32 && q_dtype != SA_DTYPE_BF16) return SA_ERR_INVALID_ARGUMENT;
+    if (Hq % Hkv) return SA_ERR_UNSUPPORTED;
+    if (!(scale == scale) || scale == INFINITY || scale == -INFINITY) return SA_ERR_INVALID_ARGUMENT;
+    if (B > 0 && (!q || !out)) return SA_ERR_INVALID_ARGUMENT;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return SA_ERR_INVALID_ARGUMENT;
+    if (sel->kind == SA_SEL_TOKENS) {
+        if (sel->k_cap < 0 || (B > 0 && sel->k_cap > 0 && (!sel->idx || !sel->count)))
+            return SA_ERR_INVALID_ARGUMENT;
+        if (B > 0 && !sel->count) return SA_ERR_INVALID_ARGUMENT;
+    } else if (sel->kind == SA_SEL_BLOCKS) {
+        if (sel->max_blocks < 0 || (B > 0 && (!sel->block_counts || (sel->max_blocks > 0 && !sel->blocks))))
+            return SA_ERR_INVALID_ARGUMENT;
+        if (!aligned(sel->blocks, 16)) return SA_ERR_INVALID_ARGUMENT;
+    } else {
+        return SA_ERR_INVALID_ARGUMENT;
+    }
+    a->q = q;
+    a->q_f32 = q_dtype == SA_DTYPE_F32;
+    a->Hq = Hq;
+    a->qscale = scale * kLog2e;
+    a->blocks = sel->kind == SA_SEL_BLOCKS;
+    a->idx = sel->idx;
+    a->cnt = sel->count;
+    a->kcap = sel->k_cap;
+    a->ent = sel->blocks;
+    a->ecnt = sel->block_counts;
+    a->max_blocks = sel->max_blocks;
     return SA_OK;
 }
 
@@ -134,7 +187,8 @@ const char *sa_status_string(sa_status s)
 
 size_t sa_workspace_bytes(sa_op op, const sa_kv_cache *kv, const sa_ws_query *q)
 {
-    if (check_cache(kv, nullptr) != SA_OK || !q) return 0;
+    const bool spans = op == SA_OP_SELECT_BLOCKS && q && q->block_args && q->block_args->mode == SA_SEL_SPANS;
+    if (check_cache(kv, nullptr, !spans) != SA_OK || !q) return 0;
     switch (op) {
     case SA_OP_SELECT_TOPK:
         if (q->num_q_heads <= 0 || q->k <= 0) return 0;
@@ -251,38 +305,13 @@ sa_status sa_sparse_decode_attn(const sa_kv_cache *kv, const void *q, sa_dtype q
     DecodeArgs a{};
     sa_status st = check_cache(kv, &a.c);
     if (st != SA_OK) return st;
-    if (num_q_heads <= 0 || !sel || num_splits < 1 || num_splits > 64) return SA_ERR_INVALID_ARGUMENT;
-    if (q_dtype != SA_DTYPE_F32 && q_dtype != SA_DTYPE_BF16) return SA_ERR_INVALID_ARGUMENT;
-    if (num_q_heads % kv->num_kv_heads) return SA_ERR_UNSUPPORTED;
-    if (!(scale == scale) || scale == INFINITY || scale == -INFINITY) return SA_ERR_INVALID_ARGUMENT;
-    if (kv->batch > 0 && (!q || !out)) return SA_ERR_INVALID_ARGUMENT;
-    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse_out, 4)) return SA_ERR_INVALID_ARGUMENT;
-    if (sel->kind == SA_SEL_TOKENS) {
-        if (sel->k_cap < 0 || (kv->batch > 0 && sel->k_cap > 0 && (!sel->idx || !sel->count)))
-            return SA_ERR_INVALID_ARGUMENT;
-        if (kv->batch > 0 && !sel->count) return SA_ERR_INVALID_ARGUMENT;
-    } else if (sel->kind == SA_SEL_BLOCKS) {
-        if (sel->max_blocks < 0 || (kv->batch > 0 && (!sel->block_counts || (sel->max_blocks > 0 && !sel->blocks))))
-            return SA_ERR_INVALID_ARGUMENT;
-        if (!aligned(sel->blocks, 16)) return SA_ERR_INVALID_ARGUMENT;
-    } else {
-        return SA_ERR_INVALID_ARGUMENT;
-    }
+    if (num_splits < 1 || num_splits > 64) return SA_ERR_INVALID_ARGUMENT;
+    st = check_decode(kv->batch, kv->num_kv_heads, q, q_dtype, num_q_heads, sel, scale, out, lse_out, &a);
+    if (st != SA_OK) return st;
     st = check_ws(ws, ws_bytes, ws_decode(kv, num_q_heads, num_splits));
     if (st != SA_OK) return st;
     char *w = static_cast<char *>(ws);
     const size_t rows = (size_t)kv->batch * num_q_heads;
-    a.q = q;
-    a.q_f32 = q_dtype == SA_DTYPE_F32;
-    a.Hq = num_q_heads;
-    a.qscale = scale * kLog2e;
-    a.blocks = sel->kind == SA_SEL_BLOCKS;
-    a.idx = sel->idx;
-    a.cnt = sel->count;
-    a.kcap = sel->k_cap;
-    a.ent = sel->blocks;
-    a.ecnt = sel->block_counts;
-    a.max_blocks = sel->max_blocks;
     a.S = num_splits;
     a.part_o = reinterpret_cast<float *>(w + kHeader);
     a.part_ml = reinterpret_cast<float *>(w + kHeader + up(rows * num_splits * kv->head_dim * sizeof(float)));
@@ -296,7 +325,7 @@ sa_status sa_select_blocks(const sa_kv_cache *kv, const sa_block_select_args *ar
                            void *ws, size_t ws_bytes, sa_stream_t stream)
 {
     CacheArgs c{};
-    sa_status st = check_cache(kv, &c);
+    sa_status st = check_cache(kv, &c, !(args && args->mode == SA_SEL_SPANS));
     if (st != SA_OK) return st;
     if (!args || !out) return SA_ERR_INVALID_ARGUMENT;
     if (args->mode == SA_SEL_SPANS) {
@@ -414,6 +443,193 @@ sa_status sa_sparse_prefill_attn(const sa_kv_cache *kv, const void *q, int32_t n
     cudaError_t e = launch_prefill(a, (cudaStream_t)stream);
     if (e == cudaErrorNotSupported) return SA_ERR_UNSUPPORTED;
     return cuda_status(e);
+}
+
+// ---------------------------------------------------------------------------
+sa_status sa_plan_append(const sa_plan_args *p, void *ws, size_t ws_bytes, sa_stream_t stream)
+{
+    if (!p || p->batch < 0 || p->max_pages_per_seq < 0 || p->num_pages < 0 || p->num_free < 0 || p->max_tokens < 0)
+        return SA_ERR_INVALID_ARGUMENT;
+    if (p->page_size != 16 && p->page_size != 64) return SA_ERR_UNSUPPORTED;
+    if (p->batch > kPlanMaxBatch || (long long)p->max_pages_per_seq * p->page_size > (1LL << 30))
+        return SA_ERR_UNSUPPORTED;
+    if (!p->free_count || !p->free_count_out || !p->cu_tokens || (p->num_free > 0 && !p->free_pages))
+        return SA_ERR_INVALID_ARGUMENT;
+    if (p->batch > 0 && (!p->seq_lens || !p->new_lens || !p->seq_lens_out ||
+                         (p->max_pages_per_seq > 0 && !p->page_table)))
+        return SA_ERR_INVALID_ARGUMENT;
+    if (p->max_tokens > 0 && (!p->positions || !p->slots)) return SA_ERR_INVALID_ARGUMENT;
+    if (!aligned(p->page_table, 4) || !aligned(p->seq_lens, 4) || !aligned(p->new_lens, 4) ||
+        !aligned(p->free_pages, 4) || !aligned(p->free_count, 4) || !aligned(p->seq_lens_out, 4) ||
+        !aligned(p->free_count_out, 4) || !aligned(p->cu_tokens, 4) || !aligned(p->positions, 4) ||
+        !aligned(p->slots, 8) || !aligned(p->seq_ids, 4))
+        return SA_ERR_INVALID_ARGUMENT;
+    sa_status st = check_ws(ws, ws_bytes, kHeader);
+    if (st != SA_OK) return st;
+    PlanArgs a{};
+    a.B = p->batch;
+    a.Plog2 = ilog2(p->page_size);
+    a.max_pages = p->max_pages_per_seq;
+    a.num_pages = p->num_pages;
+    a.num_free = p->num_free;
+    a.max_tokens = p->max_tokens;
+    a.table = p->page_table;
+    a.sl = p->seq_lens;
+    a.add = p->new_lens;
+    a.free = p->free_pages;
+    a.count = p->free_count;
+    a.sl_out = p->seq_lens_out;
+    a.count_out = p->free_count_out;
+    a.cu = p->cu_tokens;
+    a.pos = p->positions;
+    a.slots = p->slots;
+    a.seq_ids = p->seq_ids;
+    a.st = static_cast<DevStatus *>(ws);
+    return cuda_status(launch_plan(a, (cudaStream_t)stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+sa_status rope_append(const CacheArgs &c, bool kv4, const sa_append_args *p, void *ws, size_t ws_bytes,
+                      sa_stream_t stream)
+{
+    if (!p || p->num_tokens < 0 || p->num_q_heads <= 0) return SA_ERR_INVALID_ARGUMENT;
+    if (p->rot_dim < 0 || p->rot_dim > c.D || p->rot_dim % 16) return SA_ERR_INVALID_ARGUMENT;
+    if (p->weight_dtype != SA_DTYPE_F32 && p->weight_dtype != SA_DTYPE_BF16) return SA_ERR_INVALID_ARGUMENT;
+    if (!(p->eps >= 0.f) || p->eps == INFINITY) return SA_ERR_INVALID_ARGUMENT;
+    if (p->rot_dim > 0 && !p->inv_freq) return SA_ERR_INVALID_ARGUMENT;
+    if (p->num_tokens > 0 && (!p->q || !p->k || !p->v || !p->q_out || !p->positions || !p->slots || !c.k || !c.v))
+        return SA_ERR_INVALID_ARGUMENT;
+    if (!aligned(c.k, 16) || !aligned(c.v, 16)) return SA_ERR_INVALID_ARGUMENT;
+    if (p->q_stride % 8 || p->k_stride % 8 || p->v_stride % 8 || p->q_out_stride % 8) return SA_ERR_INVALID_ARGUMENT;
+    // output rows must not run into one another
+    if (p->num_tokens > 1 && p->q_out_stride < (long long)p->num_q_heads * c.D) return SA_ERR_INVALID_ARGUMENT;
+    if (p->q_out == p->q && p->num_tokens > 1 && p->q_out_stride != p->q_stride) return SA_ERR_INVALID_ARGUMENT;
+    if (!aligned(p->q, 16) || !aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->q_out, 16) ||
+        !aligned(p->q_weight, 16) || !aligned(p->k_weight, 16) || !aligned(p->positions, 4) ||
+        !aligned(p->slots, 8) || !aligned(p->inv_freq, 4))
+        return SA_ERR_INVALID_ARGUMENT;
+    sa_status st = check_ws(ws, ws_bytes, kHeader);
+    if (st != SA_OK) return st;
+    AppendArgs a{};
+    a.q = static_cast<const uint16_t *>(p->q);
+    a.k = static_cast<const uint16_t *>(p->k);
+    a.v = static_cast<const uint16_t *>(p->v);
+    a.q_stride = p->q_stride;
+    a.k_stride = p->k_stride;
+    a.v_stride = p->v_stride;
+    a.q_out_stride = p->q_out_stride;
+    a.T = p->num_tokens;
+    a.Hq = p->num_q_heads;
+    a.Hkv = c.Hkv;
+    a.D = c.D;
+    a.Plog2 = c.Plog2;
+    a.num_slots = (long long)c.num_pages << c.Plog2;
+    a.pos = p->positions;
+    a.slots = p->slots;
+    a.inv_freq = p->inv_freq;
+    a.rot = p->rot_dim;
+    a.interleaved = p->interleaved != 0;
+    a.q_weight = p->q_weight;
+    a.k_weight = p->k_weight;
+    a.w_f32 = p->weight_dtype == SA_DTYPE_F32;
+    a.eps = p->eps;
+    a.q_out = static_cast<uint16_t *>(p->q_out);
+    if (kv4) {
+        a.kv4 = reinterpret_cast<uint8_t *>(const_cast<uint16_t *>(c.k));
+    } else {
+        a.kp = const_cast<uint16_t *>(c.k);
+        a.vp = const_cast<uint16_t *>(c.v);
+    }
+    a.st = static_cast<DevStatus *>(ws);
+    return cuda_status(launch_append(a, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+sa_status sa_rope_append(const sa_kv_cache *kv, const sa_append_args *p, void *ws, size_t ws_bytes, sa_stream_t stream)
+{
+    CacheArgs c{};
+    sa_status st = check_cache(kv, &c);
+    return st != SA_OK ? st : rope_append(c, false, p, ws, ws_bytes, stream);
+}
+
+sa_status sa_rope_append_kv4(const sa_kv4_cache *kv, const sa_append_args *p, void *ws, size_t ws_bytes,
+                             sa_stream_t stream)
+{
+    CacheArgs c{};
+    sa_status st = check_cache4(kv, &c);
+    return st != SA_OK ? st : rope_append(c, true, p, ws, ws_bytes, stream);
+}
+
+sa_status sa_expand_kv4(const sa_kv4_cache *kv, const int32_t *pages, int32_t n, void *k_out, void *v_out, void *ws,
+                        size_t ws_bytes, sa_stream_t stream)
+{
+    CacheArgs c{};
+    sa_status st = check_cache4(kv, &c);
+    if (st != SA_OK) return st;
+    if (n < 0 || (n > 0 && (!pages || !k_out || !v_out || !kv->kv))) return SA_ERR_INVALID_ARGUMENT;
+    if (!aligned(kv->kv, 16) || !aligned(pages, 4) || !aligned(k_out, 16) || !aligned(v_out, 16))
+        return SA_ERR_INVALID_ARGUMENT;
+    st = check_ws(ws, ws_bytes, kHeader);
+    if (st != SA_OK) return st;
+    ExpandArgs a{};
+    a.kv4 = static_cast<const uint8_t *>(kv->kv);
+    a.pages = pages;
+    a.n = n;
+    a.Hkv = c.Hkv;
+    a.D = c.D;
+    a.Plog2 = c.Plog2;
+    a.num_pages = c.num_pages;
+    a.k = static_cast<uint16_t *>(k_out);
+    a.v = static_cast<uint16_t *>(v_out);
+    a.st = static_cast<DevStatus *>(ws);
+    return cuda_status(launch_expand(a, (cudaStream_t)stream));
+}
+
+size_t sa_kv4_decode_workspace_bytes(const sa_kv4_cache *kv, int32_t num_q_heads, int32_t num_splits)
+{
+    if (check_cache4(kv, nullptr) != SA_OK || num_q_heads <= 0 || num_splits < 0 || num_splits > 64) return 0;
+    if (num_q_heads % kv->num_kv_heads) return 0;
+    sa_kv_cache as{};
+    as.batch = kv->batch;
+    as.head_dim = kv->head_dim;
+    const int most = num_splits > 0 ? num_splits : decode_kv4_splits(kv->batch, kv4_group_rows(kv, num_q_heads), 1LL << 31);
+    return sa::decode_workspace_bytes(&as, num_q_heads, most);
+}
+
+sa_status sa_sparse_decode_attn_kv4(const sa_kv4_cache *kv, const void *q, sa_dtype q_dtype, int32_t num_q_heads,
+                                    const sa_selection *sel, float scale, int32_t num_splits, void *out,
+                                    float *lse_out, void *ws, size_t ws_bytes, sa_stream_t stream)
+{
+    DecodeArgs a{};
+    sa_status st = check_cache4(kv, &a.c);
+    if (st != SA_OK) return st;
+    if (num_splits < 0 || num_splits > 64) return SA_ERR_INVALID_ARGUMENT;
+    st = check_decode(kv->batch, kv->num_kv_heads, q, q_dtype, num_q_heads, sel, scale, out, lse_out, &a);
+    if (st != SA_OK) return st;
+    if (kv->batch > 65535 || num_q_heads > 65535) return SA_ERR_UNSUPPORTED;   // grid dimensions
+    st = check_ws(ws, ws_bytes, sa_kv4_decode_workspace_bytes(kv, num_q_heads, num_splits));
+    if (st != SA_OK) return st;
+    if (num_splits == 0) {
+        // (a token list has a CTA per query head, so never more splits than the workspace was sized for)
+        num_splits = a.blocks ? decode_kv4_splits(kv->batch, kv4_group_rows(kv, num_q_heads),
+                                                  (long long)a.max_blocks * kv->page_size)
+                              : decode_kv4_splits(kv->batch, num_q_heads, a.kcap);
+    }
+    char *w = static_cast<char *>(ws);
+    const size_t rows = (size_t)kv->batch * num_q_heads;
+    a.S = num_splits;
+    a.part_o = reinterpret_cast<float *>(w + kHeader);
+    a.part_ml = reinterpret_cast<float *>(w + kHeader + up(rows * num_splits * kv->head_dim * sizeof(float)));
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse_out;
+    a.st = static_cast<DevStatus *>(ws);
+    return cuda_status(launch_decode_kv4(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

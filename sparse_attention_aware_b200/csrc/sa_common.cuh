@@ -32,7 +32,10 @@ enum Check : unsigned {
     CHK_CAPACITY_BLOCKS = 8,// block-list capacity exceeded
     CHK_SPAN = 9,           // span count outside [0, max_spans]
     CHK_TOPK_SCRATCH = 10,  // top-k candidate buffer overflow
-    CHK_WAIT = 11           // bounded wait expired
+    CHK_WAIT = 11,          // bounded wait expired
+    CHK_SLOT = 12,          // cache slot outside [-1, num_pages*P)
+    CHK_CAPACITY_TOKENS = 13, // a step's tokens exceed max_tokens
+    CHK_CAPACITY_PAGES = 14   // a step needs more pages than are free (or frees more than the stack holds)
 };
 
 __device__ __forceinline__ void record(DevStatus *st, sa_status code, unsigned chk, int value)

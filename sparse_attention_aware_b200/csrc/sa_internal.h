@@ -58,6 +58,10 @@ cudaError_t launch_fetch(const FetchArgs &a, cudaStream_t s);
 // (split, kv head, sequence) on mma.sync (k_decode_gqa.cu)
 bool decode_gqa_supported(const DecodeArgs &a);
 cudaError_t launch_decode_gqa_split(const DecodeArgs &a, cudaStream_t s);
+// decode over a 4-bit cache (k_decode_kv4.cu): a.c.k holds the records
+cudaError_t launch_decode_kv4(const DecodeArgs &a, cudaStream_t s);
+// its split count for `rows` CTAs per (sequence, split) and lists of up to `list` tokens
+int decode_kv4_splits(int B, int rows, long long list);
 
 // ---- top-k ------------------------------------------------------------------
 struct TopkArgs {
@@ -155,5 +159,53 @@ struct PrefillArgs {
 // number of prefill work items (two 64-row halves each) for a problem
 int prefill_items(int Hq, int Hkv, int nQB);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t s);
+
+// ---- a step's pages and slots ---------------------------------------------------
+constexpr int kPlanMaxBatch = 4096;
+struct PlanArgs {
+    int B, Plog2, max_pages, num_pages, num_free, max_tokens;
+    int32_t *table;           // [B][max_pages], fresh entries written
+    const int32_t *sl, *add;  // [B]
+    int32_t *free;            // [num_free] stack
+    const int32_t *count;     // [1]
+    int32_t *sl_out, *count_out;
+    int32_t *cu;              // [B + 1]
+    int32_t *pos;             // [max_tokens]
+    int64_t *slots;           // [max_tokens]
+    int32_t *seq_ids;         // [max_tokens] or null
+    DevStatus *st;
+};
+cudaError_t launch_plan(const PlanArgs &a, cudaStream_t s);
+
+// ---- norm, rotary positions, store into the cache -------------------------------
+struct AppendArgs {
+    const uint16_t *q, *k, *v;
+    long long q_stride, k_stride, v_stride, q_out_stride;   // elements
+    int T, Hq, Hkv, D, Plog2;
+    long long num_slots;      // num_pages * P
+    const int32_t *pos;
+    const int64_t *slots;
+    const float *inv_freq;
+    int rot;
+    bool interleaved;
+    const void *q_weight, *k_weight;   // null: no norm
+    bool w_f32;
+    float eps;
+    uint16_t *q_out;
+    uint16_t *kp, *vp;        // bf16 pages, or
+    uint8_t *kv4;             // 4-bit records
+    DevStatus *st;
+};
+cudaError_t launch_append(const AppendArgs &a, cudaStream_t s);
+
+// ---- 4-bit pages back to bf16 ----------------------------------------------------
+struct ExpandArgs {
+    const uint8_t *kv4;
+    const int32_t *pages;
+    int n, Hkv, D, Plog2, num_pages;
+    uint16_t *k, *v;
+    DevStatus *st;
+};
+cudaError_t launch_expand(const ExpandArgs &a, cudaStream_t s);
 
 }  // namespace sa
