@@ -560,8 +560,9 @@ SA_API sa_status sa_expand_kv4(const sa_kv4_cache *kv, const int32_t *pages, int
 /*
  * What sa_sparse_decode_attn computes, over the values a 4-bit cache stands
  * for: same selections, outputs and errors.  Scores are accumulated in fp32 (an
- * fp32 query as bf16 high + low parts); a softmax weight times its row's scale
- * enters the P.V product as bf16.
+ * fp32 query enters as two fp16 parts, 22 bits); a softmax weight times its
+ * row's scale enters the P.V product as fp16, scaled by a power of two.  A selected row that was stored as NaN makes
+ * the outputs of its heads NaN.
  *   num_splits in [0, 64]; 0 lets the library choose from the sizes.
  *   ws  workspace of sa_kv4_decode_workspace_bytes(...) bytes
  */

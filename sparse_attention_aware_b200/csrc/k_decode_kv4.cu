@@ -9,62 +9,79 @@
 // "四、从外卖到AI": SplitKV-and-Combine).  A row of 128 channels is 144 bytes
 // here instead of 512.
 //
-// Mathematics.  A code c enters the matrix instruction as the bf16 number
-// u = 1 + c/16: its four bits are or'd below 1.0's exponent, so widening costs
-// a shift and one logic operation for two codes and no conversion.  Scale s
-// and zero z of a half row then act outside the product:
-//   x = z + s c = 16 s u + (z - 16 s)
-//   q . k = sum over halves of  16 s (q . u) + (z - 16 s) sum(q)
-//   sum_t p_t v_t = sum_t p'_t u_t - sum_t p'_t + sum_t p_t z_t,
-//                   p'_t = bf16(16 s_t p_t)
-// sum(q) comes from a product with ones of the very bf16 parts of q that the
-// first product uses, and sum p' likewise from the rounded p', so the offset
-// 1 of u cancels but for fp32 sums and the rounding of p' acts on the codes'
-// part of v alone (bf16: half a step, 2^-8 relative).
+// Mathematics.  A code c enters the matrix instruction as the fp16 number
+// u = c - 8.  With x = z + s c = s u + z', z' = z + 8 s, for each half row
+//   q . k = sum over halves of  s (q . u) + z' sum(q)
+//   sum_t p_t v_t = sum_t p'_t u_t + sum_t p_t z'_t,     p'_t = fp16(s_t p_t)
+// so scales and zeros act outside the products, and sum(q) comes from a
+// product with ones of the very fp16 parts of q that the first product uses.
+// Widening: two codes of a register are or'd into the mantissas of 1024.0 and
+// one fp16 fma takes the offset off (exact).  fp16 mantissas take a nibble at
+// bits 0-3 and at bits 4-7 alike, so 8 codes cost one shift, 4 logic
+// operations and 4 fmas on another pipe; as bf16 1 + c/16 they cost 4 shifts
+// and 4 logic operations, all on the integer pipe that bounded the kernel (67%
+// busy at 146 us for 355 MB of records).
+//
+// Ranges.  A query is scaled by a power of two per head so that its largest
+// element lies in [2^9, 2^10): fp16 then holds a bf16 query exactly down to
+// 2^-34 of that element, and an fp32 query in two parts to 2^-22.  s_t p_t is
+// scaled by a power of two per half (raised scales rescale the sums, as a
+// raised maximum does) to at most 2^15: a weight keeps 11 bits down to 2^-21
+// of the largest scale seen, 8 to 2^-24, and is within 2^-32 of that scale
+// below.  Rounding weights to fp16 keeps the error at that of the output's own
+// rounding (1.7e-3 of the norm; with bf16 weights it was 2.4e-3).
 //
 // One CTA = (split, kv head and up to 16 of its query heads -- or one query
 // head for token lists --, sequence), kDW warps that run independently until
-// the final merge.  A warp streams tiles of 16 rows through its own ring of
-// kDST shared-memory stages by bulk copies (one copy per page segment, one
-// per row of a token list), each stage on its own mbarrier with a bounded
-// wait.  Rows are padded by their scales, so 8-row matrix loads touch 32
-// distinct banks (kv4.cuh).  Per tile: S^T = K Q^T with the 16 tokens as M and
-// the heads as N of m16n8k16, softmax per head column in the base-2 domain,
-// P'^T into the B layout by movmatrix, O^T += V^T P'^T.
+// the final merge.  A warp streams stages of 32 rows through its own ring of
+// kDST shared-memory buffers by 16-byte asynchronous copies, one commit group
+// a stage: a token list's rows are gathered 3 (or 6) rows an instruction with
+// 9 (or 5) lanes a row; page segments are copied as the contiguous bytes they
+// are.  (One bulk copy per row of a list costs more instructions: each lane's
+// copy is issued on its own.)  What a stage copies is resolved -- list entry,
+// page table, row -- two steps ahead, so the ring never waits for that chain.
+// Rows are padded by their scales, so 8-row matrix loads touch 32 distinct
+// banks (kv4.cuh).  Per 16 rows: S^T = K Q^T with the tokens as M and the heads
+// as N of m16n8k16, softmax per head column in the base-2 domain, P'^T into the
+// B layout by movmatrix, O^T += V^T P'^T.
 //
 // The running maximum of a head is raised (and its sums rescaled) only when a
-// score passes it by more than 2^8: weights stay below 2^8, far from any
-// overflow, and most tiles need neither the max across lanes nor a rescale.
+// score passes it by more than 8 in the base-2 domain: weights stay below 2^8,
+// and most tiles need neither the max across lanes nor a rescale.
 //
 // Bound: HBM for long lists; the widening and the softmax take about 60% of
 // the issue slots at that rate.
-#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "kv4.cuh"
-#include "tc_ptx.cuh"
 
 namespace sa {
 namespace {
 
 constexpr int kDW = 4;                   // warps per CTA
 constexpr int kDThreads = kDW * 32;
-constexpr int kDR = 16;                  // rows per tile (the MMA's M)
-constexpr int kDST = 4;                  // ring stages per warp
-constexpr int kDWindow = 1024;           // token-list positions resolved at a time
+constexpr int kDR = 32;                  // rows per stage (two of the MMA's M)
+constexpr int kDST = 3;                  // ring stages per warp
 constexpr float kLazy = 8.f;             // log2 of how far a score may pass the running maximum
-constexpr uint64_t kDWaitNs = 1000ull * 1000 * 1000;   // 1 s
 
 template <int D>
 struct DSmem {
     static constexpr int STAGE = kDR * Kv4<D>::REC;
     static constexpr int RING = kDW * kDST * STAGE;
     static constexpr int MERGE = kDW * (16 * D + 32) * 4;   // per-warp O, m, l (up to 16 heads)
-    static constexpr int BODY = RING > MERGE ? RING : MERGE;
-    static constexpr int BARS = BODY;                        // mbarriers
-    static constexpr int ROWS = BARS + kDW * kDST * 8 + 16;  // abort flag in between; then row numbers
-    static constexpr int BYTES = ROWS;
-    static constexpr int BYTES_TOKENS = ROWS + kDWindow * 4;
+    static constexpr int BYTES = RING > MERGE ? RING : MERGE;
 };
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
 {
@@ -85,55 +102,96 @@ __device__ __forceinline__ uint32_t movm(uint32_t x)
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// D (16x8 fp32) += A (16x16 bf16, row) * B (16x8 bf16, col)
+// D (16x8 fp32) = A (16x16 fp16, row) * B (16x8 fp16, col)
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// D (16x8 fp32) += A (16x16 fp16, row) * B (16x8 fp16, col)
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1)
 {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// nibble I of each 16-bit half of w as the bf16 pair 1 + c/16
-template <int I>
-__device__ __forceinline__ uint32_t widen(uint32_t w)
-{
-    const uint32_t x = I == 0 ? w << 3 : w >> (4 * I - 3);
-    return (x & 0x00780078u) | 0x3f803f80u;
-}
-constexpr uint32_t kOnes = 0x3f803f80u;
+// Constants of widen(), kept in registers: as immediates, an and and an or of
+// two constants are two instructions.
+struct Widen {
+    uint32_t lo, hi, top, one, sixteenth, off0, off1;
+    __device__ __forceinline__ Widen()
+    {
+        asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(lo));
+        asm volatile("mov.b32 %0, 0x00f000f0;" : "=r"(hi));
+        asm volatile("mov.b32 %0, 0x64006400;" : "=r"(top));         // 1024
+        asm volatile("mov.b32 %0, 0x3c003c00;" : "=r"(one));
+        asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(sixteenth));
+        asm volatile("mov.b32 %0, 0xe408e408;" : "=r"(off0));        // -1032
+        asm volatile("mov.b32 %0, 0xd480d480;" : "=r"(off1));        // -72
+    }
+    static __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t a, uint32_t o)
+    {
+        uint32_t y;
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(a), "r"(o));
+        return y;
+    }
+    static __device__ __forceinline__ uint32_t fma2(uint32_t x, uint32_t a, uint32_t o)
+    {
+        uint32_t y;
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(a), "r"(o));
+        return y;
+    }
+    // the 8 codes of a word as 4 fp16 pairs u = c - 8: f[i] holds nibble i of
+    // the low half word (low) and of the high half word (high)
+    __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&f)[4]) const
+    {
+        const uint32_t x = w >> 8;
+        f[0] = fma2(and_or(w, lo, top), one, off0);          // 1024 + c
+        f[1] = fma2(and_or(w, hi, top), sixteenth, off1);    // 1024 + 16 c
+        f[2] = fma2(and_or(x, lo, top), one, off0);
+        f[3] = fma2(and_or(x, hi, top), sixteenth, off1);
+    }
+};
+constexpr uint32_t kOnes = 0x3c003c00u;
 
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi)
 {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    const __half2 p = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-// Query channels c0 and c1 of one head: bf16 pair, and for an fp32 query the
-// pair of the rest x - bf16(x) (so that the two carry ~16 bits of it)
-template <bool QF32>
-__device__ __forceinline__ void query_pair(const void *q, size_t row, bool valid, int c0, int c1, uint32_t &hi,
-                                           uint32_t &lo)
+// 2^e as a float, e clamped to what a float holds
+__device__ __forceinline__ float pow2(int e) { return __int_as_float(min(max(e + 127, 1), 254) << 23); }
+__device__ __forceinline__ int exponent(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
+
+// 8 query channels from element i on (a multiple of 8)
+template <bool F32>
+__device__ __forceinline__ void query8(const void *q, size_t i, float (&x)[8])
 {
-    hi = lo = 0u;
-    if (!valid) return;
-    if (QF32) {
-        const float *p = static_cast<const float *>(q) + row;
-        const float x = p[c0], y = p[c1];
-        hi = pack_pair(x, y);
-        lo = pack_pair(x - bf_lo(hi), y - bf_hi(hi));
+    if (F32) {
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(q) + i);
+        const float4 u = __ldg(p), v = __ldg(p + 1);
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
     } else {
-        const uint16_t *p = static_cast<const uint16_t *>(q) + row;
-        hi = (uint32_t)p[c0] | ((uint32_t)p[c1] << 16);
+        const uint4 w = ldg_nc_v4(static_cast<const uint16_t *>(q) + i);
+        x[0] = bf_lo(w.x); x[1] = bf_hi(w.x); x[2] = bf_lo(w.y); x[3] = bf_hi(w.y);
+        x[4] = bf_lo(w.z); x[5] = bf_hi(w.z); x[6] = bf_lo(w.w); x[7] = bf_hi(w.w);
     }
 }
 
 // NH = 8-head column blocks of the CTA (1 or 2); TOKENS: one query head and
 // its token list, else a kv head's heads and the sequence's block list
 template <int D, int NH, bool QF32, bool TOKENS>
-__global__ void __launch_bounds__(kDThreads) k_decode_kv4(const DecodeArgs a)
+__global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const DecodeArgs a)
 {
     pdl_wait();
     pdl_trigger();
@@ -141,12 +199,9 @@ __global__ void __launch_bounds__(kDThreads) k_decode_kv4(const DecodeArgs a)
     constexpr int REC = Kv4<D>::REC;
     constexpr int CB = D / 32;           // 16-byte column blocks of a row's codes (32 channels each)
     constexpr int CBH = CB / 2;          // of a half
-    constexpr int NQ = QF32 ? 2 : 1;
+    constexpr int NQ = QF32 ? 2 : 1;     // fp16 parts of the query
     extern __shared__ __align__(128) uint8_t sm[];
     const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(sm);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + SM::BARS);   // [kDW][kDST]
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + kDW * kDST);
-    uint32_t *s_row = reinterpret_cast<uint32_t *>(sm + SM::ROWS);   // token lists: rows of a window
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gq = lane >> 2, tq = lane & 3;   // mma group id / thread in group
@@ -179,7 +234,7 @@ __global__ void __launch_bounds__(kDThreads) k_decode_kv4(const DecodeArgs a)
             n = n < 0 ? 0 : a.kcap;
         }
         idx = a.idx + r * a.kcap;
-        const int chunk = ((n + a.S - 1) / a.S + kDR - 1) / kDR * kDR;   // whole tiles
+        const int chunk = ((n + a.S - 1) / a.S + kDR - 1) / kDR * kDR;   // whole stages
         lo = min(s * chunk, n);
         hi = min(lo + chunk, n);
     } else {
@@ -201,29 +256,44 @@ __global__ void __launch_bounds__(kDThreads) k_decode_kv4(const DecodeArgs a)
         return;
     }
 
-    if (tid == 0) {
-        for (int i = 0; i < kDW * kDST; ++i) tc::mbar_init(bars + i, 1);
-        *abort_flag = 0;
-        tc::fence_mbar_init();
-    }
-
     // query B fragments: column n is head h0 + n; the k-steps' channels follow
     // the order in which widen() hands out a code word (channels i and i + 4)
     uint32_t qb[NQ][NH][CB][2][2];
-    float qs[2][NH][2];   // sum of the query over each half, heads nh*8 + 2tq + j
+    float qs[2][NH][2];   // sum of the scaled query over each half, heads nh*8 + 2tq + j
+    float kf[NH][2];      // scores' factor of those heads: scale log2(e) / the query's power of two
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
         const int h = nh * 8 + gq;
-        const size_t r = ((size_t)b * a.Hq + h0 + h) * D;
+        const size_t r = ((size_t)b * a.Hq + h0 + h) * D + tq * 8;
+        float x[CB][8], top = 0.f;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[cb][i] = 0.f;
+            if (h < nheads) query8<QF32>(a.q, r + cb * 32, x[cb]);
+        }
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[cb][i]));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        const float up = pow2(9 - exponent(top));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) kf[nh][j] = a.qscale / __shfl_sync(~0u, up, (2 * tq + j) * 4);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t x, y;
-                const int c = cb * 32 + tq * 8 + i;
-                query_pair<QF32>(a.q, r, h < nheads, c, c + 4, x, y);
-                qb[0][nh][cb][i >> 1][i & 1] = x;
-                if (QF32) qb[NQ - 1][nh][cb][i >> 1][i & 1] = y;
+                float y = x[cb][i] * up, z = x[cb][i + 4] * up;
+#pragma unroll
+                for (int qi = 0; qi < NQ; ++qi) {
+                    const uint32_t part = pack_pair(y, z);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&part));
+                    y -= f.x;
+                    z -= f.y;
+                    qb[qi][nh][cb][i >> 1][i & 1] = part;
+                }
             }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -239,13 +309,11 @@ __global__ void __launch_bounds__(kDThreads) k_decode_kv4(const DecodeArgs a)
             qs[half][nh][1] = sum[1];
         }
     }
-    __syncthreads();   // mbarriers initialised
-
     // O^T fragments: o[cb][j][nh]: rows gq / gq + 8 are channels cb*32 + 4gq + 2j / + 1, columns heads 2tq, 2tq + 1
     float o[CB][2][NH][4];
-    float op[2][NH][4];            // sum of p' per half (every row the same)
-    float zs[2][NH][2];            // sum of p z per half, this thread's tokens
+    float zs[2][NH][2];            // sum of p z' per half, this thread's tokens
     float mh[NH][2], lh[NH][2];    // heads nh*8 + 2tq + j (l: this thread's tokens)
+    float mz[NH][2];               // mh, 0 for a head without a score
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
 #pragma unroll
@@ -253,41 +321,37 @@ __global__ void __launch_bounds__(kDThreads) k_decode_kv4(const DecodeArgs a)
 #pragma unroll
             for (int j = 0; j < 2; ++j) o[cb][j][nh][0] = o[cb][j][nh][1] = o[cb][j][nh][2] = o[cb][j][nh][3] = 0.f;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            op[half][nh][0] = op[half][nh][1] = op[half][nh][2] = op[half][nh][3] = 0.f;
-            zs[half][nh][0] = zs[half][nh][1] = 0.f;
-        }
+        for (int half = 0; half < 2; ++half) zs[half][nh][0] = zs[half][nh][1] = 0.f;
         mh[nh][0] = mh[nh][1] = -INFINITY;
+        mz[nh][0] = mz[nh][1] = 0.f;
         lh[nh][0] = lh[nh][1] = 0.f;
     }
 
-    uint64_t *wbar = bars + warp * kDST;
-    uint8_t *wring = sm + warp * kDST * SM::STAGE;
-    const uint32_t wring_a = sbase + warp * kDST * SM::STAGE;
-    const uint64_t deadline = tc::globaltimer() + kDWaitNs;
-    int done = 0;          // tiles this warp has consumed (stage = done % kDST, parity = (done / kDST) & 1)
-    bool alive = true;
+    // per half: the largest value scale that fits, and the power of two p s is kept at
+    float smax[2] = {pow2(-100), pow2(-100)}, keep[2] = {pow2(107), pow2(107)};
 
-    // one tile whose rows (those in `mask`) are in stage `stage`
-    auto consume = [&](int stage, uint32_t mask) {
-        const uint32_t base = wring_a + stage * SM::STAGE;
-        const uint32_t quad = base + ((lane & 7) + ((lane >> 3) & 1) * 8) * REC + (lane >> 4) * 16;
-        const uint8_t *gen = wring + stage * SM::STAGE;
-        const bool ok0 = (mask >> gq) & 1, ok1 = (mask >> (gq + 8)) & 1;
+    const Widen widen;
+    uint8_t *ring = sm + warp * kDST * SM::STAGE;
+    const uint32_t ring_a = sbase + warp * kDST * SM::STAGE;
+
+    // 16 rows (those in `mask`) at byte `at` of the ring
+    const uint32_t quad0 = ring_a + ((lane & 7) + ((lane >> 3) & 1) * 8) * REC + (lane >> 4) * 16;
+    auto consume = [&](int at, uint32_t mask) {
+        const uint32_t quad = quad0 + at;
+        const uint8_t *gen = ring + at;
         // scales and zeros {K half 0, K half 1, V half 0, V half 1} of rows gq, gq + 8; a row
         // outside the mask is whatever the stage held, and must not reach a product
         uint4 p0 = *reinterpret_cast<const uint4 *>(gen + gq * REC + Kv4<D>::PAR);
         uint4 p1 = *reinterpret_cast<const uint4 *>(gen + (gq + 8) * REC + Kv4<D>::PAR);
-        if (!ok0) p0 = make_uint4(0, 0, 0, 0);
-        if (!ok1) p1 = make_uint4(0, 0, 0, 0);
+        const bool partial = mask != 0xffffu;
+        const bool ok0 = !partial || ((mask >> gq) & 1), ok1 = !partial || ((mask >> (gq + 8)) & 1);
+        if (partial) {
+            if (!ok0) p0 = make_uint4(0, 0, 0, 0);
+            if (!ok1) p1 = make_uint4(0, 0, 0, 0);
+        }
 
         // ---- S^T = K Q^T per half
         float sc[2][NH][4];
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int nh = 0; nh < NH; ++nh)
-                sc[half][nh][0] = sc[half][nh][1] = sc[half][nh][2] = sc[half][nh][3] = 0.f;
 #pragma unroll
         for (int c2 = 0; c2 < CB; c2 += 2) {
             // matrices: rows 0-7 / 8-15 of column block c2, then of c2 + 1
@@ -295,42 +359,69 @@ __global__ void __launch_bounds__(kDThreads) k_decode_kv4(const DecodeArgs a)
             ldsm4(quad + c2 * 16, w);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint32_t w0 = w[2 * u], w1 = w[2 * u + 1];
-                const uint32_t f[2][4] = {{widen<0>(w0), widen<0>(w1), widen<1>(w0), widen<1>(w1)},
-                                          {widen<2>(w0), widen<2>(w1), widen<3>(w0), widen<3>(w1)}};
+                uint32_t f0[4], f1[4];
+                widen(w[2 * u], f0);
+                widen(w[2 * u + 1], f1);
                 const int cb = c2 + u, half = cb / CBH;
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                     for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-                        for (int qi = 0; qi < NQ; ++qi)
-                            mma(sc[half][nh], f[ks][0], f[ks][1], f[ks][2], f[ks][3], qb[qi][nh][cb][ks][0],
-                                qb[qi][nh][cb][ks][1]);
+                        for (int qi = 0; qi < NQ; ++qi) {
+                            if (cb == half * CBH && ks == 0 && qi == 0)
+                                mma0(sc[half][nh], f0[0], f1[0], f0[1], f1[1], qb[0][nh][cb][0][0], qb[0][nh][cb][0][1]);
+                            else
+                                mma(sc[half][nh], f0[2 * ks], f1[2 * ks], f0[2 * ks + 1], f1[2 * ks + 1],
+                                    qb[qi][nh][cb][ks][0], qb[qi][nh][cb][ks][1]);
+                        }
             }
         }
         // ---- scores: rows gq (elements 0, 1) and gq + 8 (2, 3), base-2 domain
-        const float k16 = 16.f * a.qscale;
-        const float s00 = bf_lo(p0.x) * k16, s01 = bf_lo(p0.y) * k16, s10 = bf_lo(p1.x) * k16, s11 = bf_lo(p1.y) * k16;
-        const float c00 = fmaf(bf_hi(p0.x), a.qscale, -s00), c01 = fmaf(bf_hi(p0.y), a.qscale, -s01);
-        const float c10 = fmaf(bf_hi(p1.x), a.qscale, -s10), c11 = fmaf(bf_hi(p1.y), a.qscale, -s11);
-        float x[NH][4];
-        bool high = false;
+        const float s00 = bf_lo(p0.x), s01 = bf_lo(p0.y), s10 = bf_lo(p1.x), s11 = bf_lo(p1.y);
+        const float c00 = fmaf(8.f, s00, bf_hi(p0.x)), c01 = fmaf(8.f, s01, bf_hi(p0.y));
+        const float c10 = fmaf(8.f, s10, bf_hi(p1.x)), c11 = fmaf(8.f, s11, bf_hi(p1.y));
+        const float v00 = bf_lo(p0.z), v01 = bf_lo(p0.w), v10 = bf_lo(p1.z), v11 = bf_lo(p1.w);
+        float x[NH][4], above = -INFINITY;
 #pragma unroll
-        for (int nh = 0; nh < NH; ++nh) {
+        for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float y0 = fmaf(s00, sc[0][nh][j], fmaf(s01, sc[1][nh][j],
-                                      fmaf(c00, qs[0][nh][j], c01 * qs[1][nh][j])));
-                const float y1 = fmaf(s10, sc[0][nh][2 + j], fmaf(s11, sc[1][nh][2 + j],
-                                      fmaf(c10, qs[0][nh][j], c11 * qs[1][nh][j])));
-                x[nh][j] = ok0 ? y0 : -INFINITY;
-                x[nh][2 + j] = ok1 ? y1 : -INFINITY;
-                // (also true for the first finite score of a head)
-                high = high || fmaxf(x[nh][j], x[nh][2 + j]) > mh[nh][j] + kLazy;
+                x[nh][j] = kf[nh][j] * fmaf(s00, sc[0][nh][j], fmaf(s01, sc[1][nh][j],
+                                            fmaf(c00, qs[0][nh][j], c01 * qs[1][nh][j])));
+                x[nh][2 + j] = kf[nh][j] * fmaf(s10, sc[0][nh][2 + j], fmaf(s11, sc[1][nh][2 + j],
+                                                fmaf(c10, qs[0][nh][j], c11 * qs[1][nh][j])));
             }
+        if (partial) {
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (!ok0) x[nh][j] = -INFINITY;
+                    if (!ok1) x[nh][2 + j] = -INFINITY;
+                }
         }
-        if (__any_sync(~0u, high)) {
+        // (the difference is +inf for the first score of a head, NaN, which
+        // compares false, while it has none)
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) above = fmaxf(above, fmaxf(x[nh][j], x[nh][2 + j]) - mh[nh][j]);
+        if (__any_sync(~0u, above > kLazy || fmaxf(v00, v10) > smax[0] || fmaxf(v01, v11) > smax[1])) {
+            float re[2] = {1.f, 1.f};   // what the halves' sums are rescaled by
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float m = half ? fmaxf(v01, v11) : fmaxf(v00, v10);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, off));
+                if (m > smax[half]) {
+                    const int e = exponent(m) + 1;   // m < 2^e
+                    smax[half] = e > 127 ? INFINITY : pow2(e);
+                    const float was = keep[half];
+                    keep[half] = pow2(7 - e);
+                    re[half] = keep[half] / was;
+                }
+            }
 #pragma unroll
             for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
@@ -340,45 +431,39 @@ __global__ void __launch_bounds__(kDThreads) k_decode_kv4(const DecodeArgs a)
                     for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, off));
                     const float al = m == -INFINITY ? 1.f : ex2(mh[nh][j] - m);   // 0 for a head that was empty
                     mh[nh][j] = m;
+                    mz[nh][j] = m == -INFINITY ? 0.f : m;
                     lh[nh][j] *= al;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        zs[half][nh][j] *= al;
-                        op[half][nh][j] *= al;
-                        op[half][nh][2 + j] *= al;
-                    }
+                    zs[0][nh][j] *= al;
+                    zs[1][nh][j] *= al;
 #pragma unroll
                     for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            o[cb][i][nh][j] *= al;
-                            o[cb][i][nh][2 + j] *= al;
+                            o[cb][i][nh][j] *= al * re[cb / CBH];
+                            o[cb][i][nh][2 + j] *= al * re[cb / CBH];
                         }
                 }
         }
         // ---- weights; P'^T (tokens x heads) per half as B fragments (k = tokens)
-        const float v00 = 16.f * bf_lo(p0.z), v01 = 16.f * bf_lo(p0.w), v10 = 16.f * bf_lo(p1.z), v11 = 16.f * bf_lo(p1.w);
-        const float z00 = bf_hi(p0.z), z01 = bf_hi(p0.w), z10 = bf_hi(p1.z), z11 = bf_hi(p1.w);
+        const float w00 = v00 * keep[0], w01 = v01 * keep[1], w10 = v10 * keep[0], w11 = v11 * keep[1];
+        const float z00 = fmaf(8.f, v00, bf_hi(p0.z)), z01 = fmaf(8.f, v01, bf_hi(p0.w));
+        const float z10 = fmaf(8.f, v10, bf_hi(p1.z)), z11 = fmaf(8.f, v11, bf_hi(p1.w));
         uint32_t pb[2][NH][2];
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh) {
             float p[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float m = mh[nh][j] == -INFINITY ? 0.f : mh[nh][j];
-                p[j] = ex2(x[nh][j] - m);
-                p[2 + j] = ex2(x[nh][2 + j] - m);
+                p[j] = ex2(x[nh][j] - mz[nh][j]);
+                p[2 + j] = ex2(x[nh][2 + j] - mz[nh][j]);
                 lh[nh][j] += p[j] + p[2 + j];
                 zs[0][nh][j] = fmaf(p[j], z00, fmaf(p[2 + j], z10, zs[0][nh][j]));
                 zs[1][nh][j] = fmaf(p[j], z01, fmaf(p[2 + j], z11, zs[1][nh][j]));
             }
-            pb[0][nh][0] = movm(pack_pair(p[0] * v00, p[1] * v00));
-            pb[0][nh][1] = movm(pack_pair(p[2] * v10, p[3] * v10));
-            pb[1][nh][0] = movm(pack_pair(p[0] * v01, p[1] * v01));
-            pb[1][nh][1] = movm(pack_pair(p[2] * v11, p[3] * v11));
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-                mma(op[half][nh], kOnes, kOnes, kOnes, kOnes, pb[half][nh][0], pb[half][nh][1]);
+            pb[0][nh][0] = movm(pack_pair(p[0] * w00, p[1] * w00));
+            pb[0][nh][1] = movm(pack_pair(p[2] * w10, p[3] * w10));
+            pb[1][nh][0] = movm(pack_pair(p[0] * w01, p[1] * w01));
+            pb[1][nh][1] = movm(pack_pair(p[2] * w11, p[3] * w11));
         }
         // ---- O^T += V^T P'^T: transposed 8x8 loads of the code bytes give, per
         // register, 4 channels of tokens 2tq (low half) and 2tq + 1 (high half)
@@ -388,162 +473,151 @@ __global__ void __launch_bounds__(kDThreads) k_decode_kv4(const DecodeArgs a)
             ldsm4_t(quad + Kv4<D>::V + c2 * 16, w);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint32_t w0 = w[2 * u], w1 = w[2 * u + 1];
-                const uint32_t f[2][4] = {{widen<0>(w0), widen<1>(w0), widen<0>(w1), widen<1>(w1)},
-                                          {widen<2>(w0), widen<3>(w0), widen<2>(w1), widen<3>(w1)}};
+                uint32_t f0[4], f1[4];
+                widen(w[2 * u], f0);
+                widen(w[2 * u + 1], f1);
                 const int cb = c2 + u, half = cb / CBH;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int nh = 0; nh < NH; ++nh)
-                        mma(o[cb][j][nh], f[j][0], f[j][1], f[j][2], f[j][3], pb[half][nh][0], pb[half][nh][1]);
+                        mma(o[cb][j][nh], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], pb[half][nh][0],
+                            pb[half][nh][1]);
             }
         }
     };
-    // waits for the warp's next stage; on expiry the warp records it and stops
-    auto arrived = [&]() -> bool {
-        const bool ok = __all_sync(~0u, tc::mbar_wait(wbar + done % kDST, (uint32_t)(done / kDST) & 1u, deadline,
-                                                      abort_flag));
-        if (!ok) {
-            *abort_flag = 1;
-            if (lane == 0) record(st, SA_ERR_TIMEOUT, CHK_WAIT, done);
-            alive = false;
-        }
-        return ok;
+    constexpr uint32_t kNone = 0xffffffffu;
+    // ring step g: its mask is kept by lane g % kDST
+    uint32_t held = 0;
+    auto hold = [&](int stage, uint32_t mask) {
+        copies_commit();
+        if (lane == stage) held = mask;
     };
-    // copies still in flight land before the CTA's shared memory is released
-    auto drain = [&](int tiles) {
-        const uint64_t dl = tc::globaltimer() + kDWaitNs;
-        volatile int zero = 0;
-        for (int i = 0; i < tiles; ++i, ++done)
-            tc::mbar_wait(wbar + done % kDST, (uint32_t)(done / kDST) & 1u, dl, &zero);
+    // consumes `steps` stages that issue(step, stage) starts, in order
+    auto stream = [&](int steps, auto &&issue) {
+        int fill = 0;
+#pragma unroll 1
+        for (; fill < kDST; ++fill) {
+            if (fill < steps) issue(fill, fill);
+            else hold(fill, 0);
+        }
+        int stage = 0;
+#pragma unroll 1
+        for (int n = 0; n < steps; ++n) {
+            copies_wait<kDST - 1>();
+            __syncwarp();   // every lane's copies of this stage are there
+            const uint32_t mask = __shfl_sync(~0u, held, stage);
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t m = t ? mask >> 16 : mask & 0xffffu;
+                if (m) consume(stage * SM::STAGE + t * 16 * REC, m);
+            }
+            __syncwarp();   // every lane is done with this stage before it is refilled
+            if (n + kDST < steps) issue(n + kDST, stage);
+            else hold(stage, 0);
+            stage = stage + 1 == kDST ? 0 : stage + 1;
+        }
     };
 
     if (TOKENS) {
-        // a window of the list is resolved (index -> page -> row, validated)
-        // into shared memory by the whole CTA; then each warp streams tiles
-        // warp, warp + kDW, ... of it
-        constexpr uint32_t kNone = 0xffffffffu;
-        for (int w0 = lo; w0 < hi; w0 += kDWindow) {
-            const int wn = min(kDWindow, hi - w0);
-            __syncthreads();   // the previous window's rows have been used
-            for (int i = tid; i < (wn + kDR - 1) / kDR * kDR; i += kDThreads) {
-                uint32_t row = kNone;
-                if (i < wn) {
-                    const int t = __ldg(idx + w0 + i);
-                    if (t < 0 || t >= L) {
-                        fault(st, CHK_INDEX, t);
-                    } else {
-                        const int page = __ldg(pt + (t >> a.c.Plog2));
-                        if (page < 0 || page >= a.c.num_pages) fault(st, CHK_PAGE, page);
-                        else row = (((uint32_t)page * a.c.Hkv + g) << a.c.Plog2) + (t & ((1 << a.c.Plog2) - 1));
-                    }
-                }
-                s_row[i] = row;
+        // step n: list positions lo + (n * kDW + warp) * 32 + lane
+        constexpr int PARTS = REC / 16, ROWS = 32 / PARTS;   // lanes of a row, rows of an instruction
+        const int part = lane % PARTS, sub = lane / PARTS;
+        const int first = lo + warp * kDR + lane;
+        const int steps = max(0, (hi - lo - warp * kDR + kDR * kDW - 1) / (kDR * kDW));
+        auto index_at = [&](int n) -> int {
+            const int i = first + n * kDR * kDW;
+            return i < hi ? __ldg(idx + i) : -1;
+        };
+        // page of token t, -1 without one (recorded)
+        auto page_of = [&](int n, int t) -> int {
+            if (first + n * kDR * kDW >= hi) return -1;
+            if (t < 0 || t >= L) {
+                fault(st, CHK_INDEX, t);
+                return -1;
             }
-            __syncthreads();
-            const int tiles = ((wn + kDR - 1) / kDR - warp + kDW - 1) / kDW;   // of this warp
-            auto issue = [&](int n, int stage) {
-                const uint32_t row = lane < kDR ? s_row[(warp + n * kDW) * kDR + lane] : kNone;
-                const uint32_t mask = __ballot_sync(~0u, row != kNone);
-                if (lane == 0) tc::mbar_arrive_expect_tx(wbar + stage, (uint32_t)__popc(mask) * REC);
-                __syncwarp();
-                if (row != kNone)
-                    tc::bulk_load(wring + stage * SM::STAGE + lane * REC, pool + (size_t)row * REC, REC, wbar + stage);
-                return mask;
-            };
-            if (!alive) continue;
-            // the masks of the tiles in flight: lane i of `held` keeps stage i's
-            uint32_t held = 0;
-            const int pre = min(tiles, kDST);
-            for (int n = 0; n < pre; ++n) {
-                const uint32_t m = issue(n, (done + n) % kDST);
-                if (lane == (done + n) % kDST) held = m;
+            return __ldg(pt + (t >> a.c.Plog2));
+        };
+        int t0 = index_at(0), t1 = index_at(1);
+        int page = page_of(0, t0);
+        stream(steps, [&](int n, int stage) {
+            uint32_t row = kNone;
+            if (first + n * kDR * kDW < hi && t0 >= 0 && t0 < L) {
+                if (page < 0 || page >= a.c.num_pages) fault(st, CHK_PAGE, page);
+                else row = (((uint32_t)page * a.c.Hkv + g) << a.c.Plog2) + (t0 & ((1 << a.c.Plog2) - 1));
             }
-            for (int n = 0; n < tiles; ++n) {
-                const int stage = done % kDST;
-                if (!arrived()) {
-                    drain(min(tiles - n, kDST));
-                    break;
-                }
-                consume(stage, __shfl_sync(~0u, held, stage));
-                ++done;
-                __syncwarp();   // every lane is done with this stage before it is refilled
-                if (n + kDST < tiles) {
-                    const uint32_t m = issue(n + kDST, stage);
-                    if (lane == stage) held = m;
-                }
-            }
-        }
-    } else {
-        // the warp's entries lo + warp + kDW * j, a window of 32 (one per lane) at a time
-        for (int wb = lo + warp; wb < hi && alive; wb += 32 * kDW) {
-            const int e = wb + kDW * lane;
-            int first = 0, len = 0;   // the entry's first row within the page, and its rows (0 = skipped)
-            uint32_t row = 0;
-            if (e < hi) {
-                const int4 en = ent[e];
-                bool ok = en.y >= 0 && en.y < en.z && en.z <= (1 << a.c.Plog2) && en.x >= 0 && en.x < a.c.max_pages;
-                if (!ok) fault(st, CHK_BLOCK_ENTRY, e);
-                if (ok && (en.x << a.c.Plog2) + en.z > L) {
-                    fault(st, CHK_INDEX, (en.x << a.c.Plog2) + en.z - 1);
-                    ok = false;
-                }
-                if (ok) {
-                    const int page = __ldg(pt + en.x);
-                    if (page < 0 || page >= a.c.num_pages) {
-                        fault(st, CHK_PAGE, page);
-                    } else {
-                        first = en.y;
-                        len = en.z - en.y;
-                        row = (((uint32_t)page * a.c.Hkv + g) << a.c.Plog2) + first;
-                    }
-                }
-            }
-            // tiles per entry, inclusive prefix over the lanes
-            const int nt = (len + kDR - 1) / kDR;
-            int incl = nt;
+            t0 = t1;
+            page = page_of(n + 1, t0);
+            t1 = index_at(n + 2);
+            const uint32_t mask = __ballot_sync(~0u, row != kNone);
+            const uint32_t dst = ring_a + stage * SM::STAGE + part * 16;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int y = __shfl_up_sync(~0u, incl, off);
-                if (lane >= off) incl += y;
+            for (int i = 0; i < (kDR + ROWS - 1) / ROWS; ++i) {
+                const int r = i * ROWS + sub;
+                const uint32_t from = __shfl_sync(~0u, row, r & 31);
+                if (sub < ROWS && r < kDR && from != kNone)
+                    copy16(dst + r * REC, pool + (size_t)from * REC + part * 16);
             }
-            const int tiles = __shfl_sync(~0u, incl, 31);
-            // tile n: rows of the entry that holds it; returns their number
-            auto issue = [&](int n, int stage) -> int {
-                const int src = __ffs(__ballot_sync(~0u, incl > n)) - 1;
-                const uint32_t r = __shfl_sync(~0u, row, src);
-                const int ln = __shfl_sync(~0u, len, src);
-                const int at = (n - __shfl_sync(~0u, incl - nt, src)) * kDR;
-                const int rows = min(kDR, ln - at);
-                if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(wbar + stage, (uint32_t)rows * REC);
-                    tc::bulk_load(wring + stage * SM::STAGE, pool + (size_t)(r + at) * REC, (uint32_t)rows * REC,
-                                  wbar + stage);
-                }
-                return rows;
-            };
-            int held = 0;   // lane i: rows of the tile in stage i
-            const int pre = min(tiles, kDST);
-            for (int n = 0; n < pre; ++n) {
-                const int r = issue(n, (done + n) % kDST);
-                if (lane == (done + n) % kDST) held = r;
+            hold(stage, mask);
+        });
+    } else {
+        // the warp's entries lo + warp + kDW * j, a window of 32 (one per lane)
+        // at a time.  A step is 32 rows of an entry of a 64-token page, or two
+        // entries of 16-token pages, 16 rows each.
+        const bool small = a.c.Plog2 == 4;
+        const int mine = (hi - lo - warp + kDW - 1) / kDW;   // entries of this warp (0 or more)
+        const int steps = small ? (mine + 1) / 2 : 2 * mine;
+        auto entry_at = [&](int w) -> int4 {
+            const int j = w * 32 + lane;
+            return j < mine ? ent[lo + warp + kDW * j] : make_int4(0, 0, 0, 0);
+        };
+        // page of an entry, -1 for one that is malformed (recorded)
+        auto page_of = [&](int w, const int4 &en) -> int {
+            if (w * 32 + lane >= mine) return -1;
+            if (en.y < 0 || en.y >= en.z || en.z > (1 << a.c.Plog2) || en.x < 0 || en.x >= a.c.max_pages) {
+                fault(st, CHK_BLOCK_ENTRY, lo + warp + kDW * (w * 32 + lane));
+                return -1;
             }
-            for (int n = 0; n < tiles; ++n) {
-                const int stage = done % kDST;
-                if (!arrived()) {
-                    drain(min(tiles - n, kDST));
-                    break;
-                }
-                consume(stage, (1u << __shfl_sync(~0u, held, stage)) - 1u);
-                ++done;
-                __syncwarp();   // every lane is done with this stage before it is refilled
-                if (n + kDST < tiles) {
-                    const int r = issue(n + kDST, stage);
-                    if (lane == stage) held = r;
-                }
+            if ((en.x << a.c.Plog2) + en.z > L) {
+                fault(st, CHK_INDEX, (en.x << a.c.Plog2) + en.z - 1);
+                return -1;
             }
-        }
+            const int page = __ldg(pt + en.x);
+            if (page < 0 || page >= a.c.num_pages) {
+                fault(st, CHK_PAGE, page);
+                return -1;
+            }
+            return page;
+        };
+        uint32_t row = 0;   // of this lane's entry of the window: its first row
+        int len = 0;        // and its rows
+        int4 e1 = make_int4(0, 0, 0, 0);
+        if (steps > 0) e1 = entry_at(0);
+        const int log_spw = small ? 4 : 6;   // log2 of steps per window
+        stream(max(steps, 0), [&](int n, int stage) {
+            const int w = n >> log_spw, i = n & ((1 << log_spw) - 1);
+            if (i == 0) {
+                const int page = page_of(w, e1);
+                len = page < 0 ? 0 : e1.z - e1.y;
+                row = (((uint32_t)max(page, 0) * a.c.Hkv + g) << a.c.Plog2) + e1.y;
+                e1 = entry_at(w + 1);
+            }
+            // rows 0-15 and 16-31 of the step: where they come from, how many
+            const int src = small ? 2 * i : i >> 1, skip = small ? 0 : (i & 1) * kDR;
+            const int la = __shfl_sync(~0u, len, src) - skip, lb = small ? __shfl_sync(~0u, len, src + 1) : la - 16;
+            const uint32_t ra = __shfl_sync(~0u, row, src) + skip, rb = small ? __shfl_sync(~0u, row, src + 1) : ra + 16;
+            const int na = min(max(la, 0), 16), nb = min(max(lb, 0), 16);
+            const uint32_t dst = ring_a + stage * SM::STAGE + lane * 16;
+            const uint8_t *pa = pool + (size_t)ra * REC + lane * 16, *pb = pool + (size_t)rb * REC + lane * 16 - 16 * REC;
+            const int ea = na * REC, eb = (16 + nb) * REC;
+#pragma unroll
+            for (int c = 0; c < (kDR * REC + 511) / 512; ++c) {
+                const int at = c * 512 + lane * 16;
+                const bool second = at >= 16 * REC;
+                if (at < (second ? eb : ea)) copy16(dst + c * 512, (second ? pb : pa) + c * 512);
+            }
+            hold(stage, ((1u << na) - 1u) | (((1u << nb) - 1u) << 16));
+        });
     }
 
     // ---- merge the warps' states through shared memory
@@ -571,7 +645,7 @@ __global__ void __launch_bounds__(kDThreads) k_decode_kv4(const DecodeArgs a)
                 for (int i = 0; i < 4; ++i) {
                     const int h = nh * 8 + 2 * tq + (i & 1), half = cb / CBH;
                     const int c = cb * 32 + 4 * gq + 2 * j + (i >> 1);
-                    mo[(warp * 16 + h) * D + c] = o[cb][j][nh][i] + (zs[half][nh][i & 1] - op[half][nh][i & 1]);
+                    mo[(warp * 16 + h) * D + c] =  fmaf(o[cb][j][nh][i], 1.f / keep[half], zs[half][nh][i & 1]);
                 }
     if (gq == 0) {
 #pragma unroll
@@ -635,7 +709,7 @@ __global__ void __launch_bounds__(D) k_kv4_combine(const float *__restrict__ par
 template <int D, int NH, bool QF32, bool TOKENS>
 cudaError_t launch_kv4(const DecodeArgs &a, cudaStream_t s)
 {
-    constexpr int smem = TOKENS ? DSmem<D>::BYTES_TOKENS : DSmem<D>::BYTES;
+    constexpr int smem = DSmem<D>::BYTES;
     auto kern = k_decode_kv4<D, NH, QF32, TOKENS>;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
     const int hpg = a.Hq / a.c.Hkv;

@@ -137,16 +137,17 @@ def decode(kv, table, q, tokens, scale):
             lse[b, h] = torch.logsumexp(z, 0)
             w = torch.exp(z - lse[b, h])
             out[b, h] = w @ v
-            # score: fp32 sums of terms up to 16 s u q and z q, d of them in 8
-            # steps (2^-23 each); an fp32 query keeps 16 of its bits
-            big = (16 * 2 * s[:, 0].amax(-1) + (k.abs().amax(-1) + 15 * s[:, 0].amax(-1))) * x.abs().sum()
-            err = float((big * 12 * 2.0 ** -23 + (k.abs() @ x.abs() * 2.0 ** -16 if f32 else 0)).max()) * abs(scale)
+            # score: fp32 sums of terms up to 8 s q and (z + 8 s) q, d of them in 8
+            # steps (2^-23 each); an fp32 query keeps 22 of its bits
+            big = (8 * s[:, 0].amax(-1) + k.abs().amax(-1) + 15 * s[:, 0].amax(-1)) * x.abs().sum()
+            err = float((big * 12 * 2.0 ** -23 + (k.abs() @ x.abs() * 2.0 ** -22 if f32 else 0)).max()) * abs(scale)
             # weights: twice the score's error, ex2 to 2^-22, the product's sums (2^-23 a tile)
             rel = 2 * err + 2.0 ** -20 + t.numel() / 16 * 2.0 ** -23
             half = s[:, 1].amax(0).repeat_interleave(d // 2)          # largest scale of either half
             top = v.abs().amax(0) + 31 * half
-            # the rounding of p' (half a bf16 step of p s, times codes up to 15), and of the output
-            tol_o[b, h] = BF16_HALF * (15 * half + out[b, h].abs()) + rel * top
+            # the rounding of s p (half an fp16 step, 2^-11, times codes up to 8 from the
+            # middle), and of the output
+            tol_o[b, h] = 2.0 ** -11 * 8 * half + BF16_HALF * out[b, h].abs() + rel * top
             tol_l[b, h] = err + 2.0 ** -20 * (1 + abs(float(lse[b, h])))
     return out, lse, tol_o, tol_l
 
