@@ -9,27 +9,28 @@
 // "四、从外卖到AI": SplitKV-and-Combine).  A row of 128 channels is 144 bytes
 // here instead of 512.
 //
-// Mathematics.  A code c enters the matrix instruction as the fp16 number
-// u = c - 8.  With x = z + s c = s u + z', z' = z + 8 s, for each half row
-//   q . k = sum over halves of  s (q . u) + z' sum(q)
-//   sum_t p_t v_t = sum_t p'_t u_t + sum_t p_t z'_t,     p'_t = fp16(s_t p_t)
+// Mathematics.  A half row is x = z + s c with codes c in [0, 15]:
+//   q . k = sum over halves of  s (q . c) + z sum(q)
+//   sum_t p_t v_t = sum_t p'_t c_t + sum_t p_t z_t,     p'_t = fp16(s_t p_t)
 // so scales and zeros act outside the products, and sum(q) comes from a
 // product with ones of the very fp16 parts of q that the first product uses.
-// Widening: two codes of a register are or'd into the mantissas of 1024.0 and
-// one fp16 fma takes the offset off (exact).  fp16 mantissas take a nibble at
-// bits 0-3 and at bits 4-7 alike, so 8 codes cost one shift, 4 logic
-// operations and 4 fmas on another pipe; as bf16 1 + c/16 they cost 4 shifts
-// and 4 logic operations, all on the integer pipe that bounded the kernel (67%
-// busy at 146 us for 355 MB of records).
+// The codes enter the matrix instruction as they are: a nibble alone in the
+// low bits of a 16-bit word is the subnormal fp16 number c 2^-24, one in bits
+// 4-7 is 16 c 2^-24, and fp16 products are exact, so eight codes cost one
+// shift and four masks.  The 16 goes into the query (a sixteenth of those
+// channels) or out of the sums (those rows of O), the 2^24 into the factors.
+// Measured at 32 sequences x 8 kv heads, 409 MB of records: 146 us with bf16
+// numbers 1 + c/16 (one logic operation and one shift a pair, all on the
+// integer pipe), 118 us with fp16 numbers c - 8 (a mask-or and an fma a pair).
 //
 // Ranges.  A query is scaled by a power of two per head so that its largest
 // element lies in [2^9, 2^10): fp16 then holds a bf16 query exactly down to
-// 2^-34 of that element, and an fp32 query in two parts to 2^-22.  s_t p_t is
-// scaled by a power of two per half (raised scales rescale the sums, as a
-// raised maximum does) to at most 2^15: a weight keeps 11 bits down to 2^-21
-// of the largest scale seen, 8 to 2^-24, and is within 2^-32 of that scale
-// below.  Rounding weights to fp16 keeps the error at that of the output's own
-// rounding (1.7e-3 of the norm; with bf16 weights it was 2.4e-3).
+// 2^-22 of that element (to 2^-30 of it below), and an fp32 query in two parts
+// to 2^-22.  s_t p_t is scaled by a power of two per half (raised scales
+// rescale the sums, as a raised maximum does) to at most 2^15: a weight keeps
+// 11 bits down to 2^-21 of the largest scale seen, 8 to 2^-24, and is within
+// 2^-32 of that scale below.  The rounding of a weight times codes of up to 15
+// steps stays below that of the bf16 output.
 //
 // One CTA = (split, kv head and up to 16 of its query heads -- or one query
 // head for token lists --, sequence), kDW warps that run independently until
@@ -61,7 +62,8 @@ namespace {
 constexpr int kDW = 4;                   // warps per CTA
 constexpr int kDThreads = kDW * 32;
 constexpr int kDR = 32;                  // rows per stage (two of the MMA's M)
-constexpr int kDST = 3;                  // ring stages per warp
+constexpr int kDST = 3;                   // ring stages per warp
+constexpr int kLeast = 256, kLong = 1024;   // tokens of a split: see split_at
 constexpr float kLazy = 8.f;             // log2 of how far a score may pass the running maximum
 
 template <int D>
@@ -123,44 +125,18 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Constants of widen(), kept in registers: as immediates, an and and an or of
-// two constants are two instructions.
-struct Widen {
-    uint32_t lo, hi, top, one, sixteenth, off0, off1;
-    __device__ __forceinline__ Widen()
-    {
-        asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(lo));
-        asm volatile("mov.b32 %0, 0x00f000f0;" : "=r"(hi));
-        asm volatile("mov.b32 %0, 0x64006400;" : "=r"(top));         // 1024
-        asm volatile("mov.b32 %0, 0x3c003c00;" : "=r"(one));
-        asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(sixteenth));
-        asm volatile("mov.b32 %0, 0xe408e408;" : "=r"(off0));        // -1032
-        asm volatile("mov.b32 %0, 0xd480d480;" : "=r"(off1));        // -72
-    }
-    static __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t a, uint32_t o)
-    {
-        uint32_t y;
-        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(a), "r"(o));
-        return y;
-    }
-    static __device__ __forceinline__ uint32_t fma2(uint32_t x, uint32_t a, uint32_t o)
-    {
-        uint32_t y;
-        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(a), "r"(o));
-        return y;
-    }
-    // the 8 codes of a word as 4 fp16 pairs u = c - 8: f[i] holds nibble i of
-    // the low half word (low) and of the high half word (high)
-    __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&f)[4]) const
-    {
-        const uint32_t x = w >> 8;
-        f[0] = fma2(and_or(w, lo, top), one, off0);          // 1024 + c
-        f[1] = fma2(and_or(w, hi, top), sixteenth, off1);    // 1024 + 16 c
-        f[2] = fma2(and_or(x, lo, top), one, off0);
-        f[3] = fma2(and_or(x, hi, top), sixteenth, off1);
-    }
-};
-constexpr uint32_t kOnes = 0x3c003c00u;
+// the 8 codes of a word as 4 fp16 pairs: f[i] holds nibble i of the low half
+// word (low) and of the high half word (high), c 2^-24 for even i, 16 c 2^-24
+// for odd i
+__device__ __forceinline__ void widen(uint32_t w, uint32_t (&f)[4])
+{
+    const uint32_t x = w >> 8;
+    f[0] = w & 0x000f000fu;
+    f[1] = w & 0x00f000f0u;
+    f[2] = x & 0x000f000fu;
+    f[3] = x & 0x00f000f0u;
+}
+constexpr uint32_t kOnes = 0x3c003c00u, kSixteens = 0x4c004c00u;   // fp16 pairs
 
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi)
 {
@@ -188,10 +164,28 @@ __device__ __forceinline__ void query8(const void *q, size_t i, float (&x)[8])
     }
 }
 
+// Where split s of a list of n begins, in units of `unit` positions.  The list
+// is cut into at most S splits of at least `least`.  Long splits (`long_` and
+// more) are cut at n (1 - (1 - s/S)^2), each smaller than the one before it:
+// CTAs are launched in order of s, so the long splits of all sequences go
+// first and the short ones fill the device's slots as they fall free (equal
+// splits left 16% of it idle at the end of a launch of ragged sequences).
+// Short ones are equal: all run at once, and the longest sets the time.
+__device__ __forceinline__ int split_at(int n, int s, int S, int least, int long_, int unit)
+{
+    S = min(S, (n + least - 1) / least);
+    if (s <= 0) return 0;
+    if (s >= S) return n;
+    // (fp32: only the order of the boundaries matters, and rounding keeps it)
+    float left = (float)(S - s) / (float)S;
+    if (n >= long_ * S) left *= left;
+    return n - min(n, ((int)((float)n * left) + unit - 1) & ~(unit - 1));
+}
+
 // NH = 8-head column blocks of the CTA (1 or 2); TOKENS: one query head and
 // its token list, else a kv head's heads and the sequence's block list
 template <int D, int NH, bool QF32, bool TOKENS>
-__global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const DecodeArgs a)
+__global__ void __launch_bounds__(kDThreads, NH == 1 ? 3 : 2) k_decode_kv4(const DecodeArgs a)
 {
     pdl_wait();
     pdl_trigger();
@@ -199,22 +193,35 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const
     constexpr int REC = Kv4<D>::REC;
     constexpr int CB = D / 32;           // 16-byte column blocks of a row's codes (32 channels each)
     constexpr int CBH = CB / 2;          // of a half
+    constexpr int TT = NH == 1 ? 2 : 1;  // 16-row tiles at a time
     constexpr int NQ = QF32 ? 2 : 1;     // fp16 parts of the query
     extern __shared__ __align__(128) uint8_t sm[];
     const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(sm);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gq = lane >> 2, tq = lane & 3;   // mma group id / thread in group
-    const int s = blockIdx.x, b = blockIdx.z;
+    const int s = blockIdx.z, b = blockIdx.y;
     const int HPG = a.Hq / a.c.Hkv;
     const int hblocks = (HPG + 15) / 16;
-    const int g = TOKENS ? blockIdx.y / HPG : blockIdx.y / hblocks;
-    const int h0 = TOKENS ? blockIdx.y : g * HPG + (blockIdx.y % hblocks) * 16;   // first query head
+    const int g = TOKENS ? blockIdx.x / HPG : blockIdx.x / hblocks;
+    const int h0 = TOKENS ? blockIdx.x : g * HPG + (blockIdx.x % hblocks) * 16;   // first query head
     const int nheads = TOKENS ? 1 : min(16, (g + 1) * HPG - h0);
     const uint8_t *pool = reinterpret_cast<const uint8_t *>(a.c.k);
     DevStatus *st = a.st;
     const bool reports = s == 0 && tid == 0;
 
+    // the query's channels first: they wait on nothing (column n is head h0 + n)
+    float qx[NH][CB][8];
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+        const int h = nh * 8 + gq;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) qx[nh][cb][i] = 0.f;
+            if (h < nheads) query8<QF32>(a.q, ((size_t)b * a.Hq + h0 + h) * D + cb * 32 + tq * 8, qx[nh][cb]);
+        }
+    }
     const int Lcap = a.c.max_pages << a.c.Plog2;
     int L = __ldg(a.c.sl + b);
     if (L < 0 || L > Lcap) {
@@ -234,9 +241,8 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const
             n = n < 0 ? 0 : a.kcap;
         }
         idx = a.idx + r * a.kcap;
-        const int chunk = ((n + a.S - 1) / a.S + kDR - 1) / kDR * kDR;   // whole stages
-        lo = min(s * chunk, n);
-        hi = min(lo + chunk, n);
+        lo = split_at(n, s, a.S, kLeast, kLong, kDR);
+        hi = split_at(n, s + 1, a.S, kLeast, kLong, kDR);
     } else {
         int n = __ldg(a.ecnt + b);
         if (n < 0 || n > a.max_blocks) {
@@ -244,8 +250,8 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const
             n = n < 0 ? 0 : a.max_blocks;
         }
         ent = reinterpret_cast<const int4 *>(a.ent) + (size_t)b * a.max_blocks;
-        lo = (int)((long long)n * s / a.S);
-        hi = (int)((long long)n * (s + 1) / a.S);
+        lo = split_at(n, s, a.S, kLeast >> a.c.Plog2, kLong >> a.c.Plog2, 1);
+        hi = split_at(n, s + 1, a.S, kLeast >> a.c.Plog2, kLong >> a.c.Plog2, 1);
     }
     if (lo >= hi) {   // nothing for this split: an empty partial, which the combine skips
         for (int j = tid; j < nheads; j += kDThreads) {
@@ -256,42 +262,35 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const
         return;
     }
 
-    // query B fragments: column n is head h0 + n; the k-steps' channels follow
-    // the order in which widen() hands out a code word (channels i and i + 4)
+    // query B fragments: the k-steps' channels follow the order in which widen() hands out a code word (channels i and i + 4)
     uint32_t qb[NQ][NH][CB][2][2];
-    float qs[2][NH][2];   // sum of the scaled query over each half, heads nh*8 + 2tq + j
-    float kf[NH][2];      // scores' factor of those heads: scale log2(e) / the query's power of two
+    constexpr float kUnit = 5.9604644775390625e-8f;   // 2^-24
+    float qs[2][NH][2];   // 2^-24 sum of the scaled query over each half, heads nh*8 + 2tq + j
+    float kf[NH][2];      // scores' factor of those heads: 2^24 scale log2(e) / the query's power of two
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
-        const int h = nh * 8 + gq;
-        const size_t r = ((size_t)b * a.Hq + h0 + h) * D + tq * 8;
-        float x[CB][8], top = 0.f;
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[cb][i] = 0.f;
-            if (h < nheads) query8<QF32>(a.q, r + cb * 32, x[cb]);
-        }
+        float top = 0.f;
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[cb][i]));
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(qx[nh][cb][i]));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
         const float up = pow2(9 - exponent(top));
 #pragma unroll
-        for (int j = 0; j < 2; ++j) kf[nh][j] = a.qscale / __shfl_sync(~0u, up, (2 * tq + j) * 4);
+        for (int j = 0; j < 2; ++j) kf[nh][j] = a.qscale / kUnit / __shfl_sync(~0u, up, (2 * tq + j) * 4);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float y = x[cb][i] * up, z = x[cb][i + 4] * up;
+                const float f = (i & 1) ? up * 0.0625f : up;   // odd nibbles stand for 16 c
+                float y = qx[nh][cb][i] * f, z = qx[nh][cb][i + 4] * f;
 #pragma unroll
                 for (int qi = 0; qi < NQ; ++qi) {
                     const uint32_t part = pack_pair(y, z);
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&part));
-                    y -= f.x;
-                    z -= f.y;
+                    const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&part));
+                    y -= r.x;
+                    z -= r.y;
                     qb[qi][nh][cb][i >> 1][i & 1] = part;
                 }
             }
@@ -304,14 +303,14 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const
                 for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                     for (int qi = 0; qi < NQ; ++qi)
-                        mma(sum, kOnes, kOnes, kOnes, kOnes, qb[qi][nh][cb][ks][0], qb[qi][nh][cb][ks][1]);
-            qs[half][nh][0] = sum[0];
-            qs[half][nh][1] = sum[1];
+                        mma(sum, kOnes, kOnes, kSixteens, kSixteens, qb[qi][nh][cb][ks][0], qb[qi][nh][cb][ks][1]);
+            qs[half][nh][0] = sum[0] * kUnit;
+            qs[half][nh][1] = sum[1] * kUnit;
         }
     }
     // O^T fragments: o[cb][j][nh]: rows gq / gq + 8 are channels cb*32 + 4gq + 2j / + 1, columns heads 2tq, 2tq + 1
     float o[CB][2][NH][4];
-    float zs[2][NH][2];            // sum of p z' per half, this thread's tokens
+    float zs[2][NH][2];            // sum of p z per half, this thread's tokens
     float mh[NH][2], lh[NH][2];    // heads nh*8 + 2tq + j (l: this thread's tokens)
     float mz[NH][2];               // mh, 0 for a head without a score
 #pragma unroll
@@ -330,88 +329,101 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const
     // per half: the largest value scale that fits, and the power of two p s is kept at
     float smax[2] = {pow2(-100), pow2(-100)}, keep[2] = {pow2(107), pow2(107)};
 
-    const Widen widen;
     uint8_t *ring = sm + warp * kDST * SM::STAGE;
     const uint32_t ring_a = sbase + warp * kDST * SM::STAGE;
 
-    // 16 rows (those in `mask`) at byte `at` of the ring
+    // TT * 16 rows (those in `mask`) at byte `at` of the ring.  The tiles are
+    // independent up to the running sums, so with a group's 8 heads two at a
+    // time hide each other's latencies.
     const uint32_t quad0 = ring_a + ((lane & 7) + ((lane >> 3) & 1) * 8) * REC + (lane >> 4) * 16;
     auto consume = [&](int at, uint32_t mask) {
-        const uint32_t quad = quad0 + at;
-        const uint8_t *gen = ring + at;
+        const bool partial = mask != (TT == 2 ? 0xffffffffu : 0xffffu);
         // scales and zeros {K half 0, K half 1, V half 0, V half 1} of rows gq, gq + 8; a row
         // outside the mask is whatever the stage held, and must not reach a product
-        uint4 p0 = *reinterpret_cast<const uint4 *>(gen + gq * REC + Kv4<D>::PAR);
-        uint4 p1 = *reinterpret_cast<const uint4 *>(gen + (gq + 8) * REC + Kv4<D>::PAR);
-        const bool partial = mask != 0xffffu;
-        const bool ok0 = !partial || ((mask >> gq) & 1), ok1 = !partial || ((mask >> (gq + 8)) & 1);
-        if (partial) {
-            if (!ok0) p0 = make_uint4(0, 0, 0, 0);
-            if (!ok1) p1 = make_uint4(0, 0, 0, 0);
-        }
+        uint4 par[TT][2];
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                par[t][r] = *reinterpret_cast<const uint4 *>(ring + at + (t * 16 + r * 8 + gq) * REC + Kv4<D>::PAR);
+                if (partial && !((mask >> (t * 16 + r * 8 + gq)) & 1)) par[t][r] = make_uint4(0, 0, 0, 0);
+            }
 
         // ---- S^T = K Q^T per half
-        float sc[2][NH][4];
+        float sc[TT][2][NH][4];
 #pragma unroll
-        for (int c2 = 0; c2 < CB; c2 += 2) {
-            // matrices: rows 0-7 / 8-15 of column block c2, then of c2 + 1
-            uint32_t w[4];
-            ldsm4(quad + c2 * 16, w);
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint32_t f0[4], f1[4];
-                widen(w[2 * u], f0);
-                widen(w[2 * u + 1], f1);
-                const int cb = c2 + u, half = cb / CBH;
+            for (int c2 = 0; c2 < CB; c2 += 2) {
+                // matrices: rows 0-7 / 8-15 of column block c2, then of c2 + 1
+                uint32_t w[4];
+                ldsm4(quad0 + at + t * 16 * REC + c2 * 16, w);
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks)
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t f0[4], f1[4];
+                    widen(w[2 * u], f0);
+                    widen(w[2 * u + 1], f1);
+                    const int cb = c2 + u, half = cb / CBH;
 #pragma unroll
-                    for (int nh = 0; nh < NH; ++nh)
+                    for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                        for (int qi = 0; qi < NQ; ++qi) {
-                            if (cb == half * CBH && ks == 0 && qi == 0)
-                                mma0(sc[half][nh], f0[0], f1[0], f0[1], f1[1], qb[0][nh][cb][0][0], qb[0][nh][cb][0][1]);
-                            else
-                                mma(sc[half][nh], f0[2 * ks], f1[2 * ks], f0[2 * ks + 1], f1[2 * ks + 1],
-                                    qb[qi][nh][cb][ks][0], qb[qi][nh][cb][ks][1]);
-                        }
+                        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                            for (int qi = 0; qi < NQ; ++qi) {
+                                if (cb == half * CBH && ks == 0 && qi == 0)
+                                    mma0(sc[t][half][nh], f0[0], f1[0], f0[1], f1[1], qb[0][nh][cb][0][0],
+                                         qb[0][nh][cb][0][1]);
+                                else
+                                    mma(sc[t][half][nh], f0[2 * ks], f1[2 * ks], f0[2 * ks + 1], f1[2 * ks + 1],
+                                        qb[qi][nh][cb][ks][0], qb[qi][nh][cb][ks][1]);
+                            }
+                }
             }
-        }
         // ---- scores: rows gq (elements 0, 1) and gq + 8 (2, 3), base-2 domain
-        const float s00 = bf_lo(p0.x), s01 = bf_lo(p0.y), s10 = bf_lo(p1.x), s11 = bf_lo(p1.y);
-        const float c00 = fmaf(8.f, s00, bf_hi(p0.x)), c01 = fmaf(8.f, s01, bf_hi(p0.y));
-        const float c10 = fmaf(8.f, s10, bf_hi(p1.x)), c11 = fmaf(8.f, s11, bf_hi(p1.y));
-        const float v00 = bf_lo(p0.z), v01 = bf_lo(p0.w), v10 = bf_lo(p1.z), v11 = bf_lo(p1.w);
-        float x[NH][4], above = -INFINITY;
+        float x[TT][NH][4], above = -INFINITY, vs[2] = {0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint4 &p = par[t][r];
+                const float s0 = bf_lo(p.x), s1 = bf_lo(p.y);
+                const float c0 = bf_hi(p.x), c1 = bf_hi(p.y);
+                vs[0] = fmaxf(vs[0], bf_lo(p.z));
+                vs[1] = fmaxf(vs[1], bf_lo(p.w));
+#pragma unroll
+                for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        x[t][nh][2 * r + j] = kf[nh][j] * fmaf(s0, sc[t][0][nh][2 * r + j],
+                                                               fmaf(s1, sc[t][1][nh][2 * r + j],
+                                                                    fmaf(c0, qs[0][nh][j], c1 * qs[1][nh][j])));
+            }
+        if (partial) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    if (!((mask >> (t * 16 + r * 8 + gq)) & 1)) {
+#pragma unroll
+                        for (int nh = 0; nh < NH; ++nh) x[t][nh][2 * r] = x[t][nh][2 * r + 1] = -INFINITY;
+                    }
+        }
+        // (the difference is +inf for the first score of a head, NaN, which
+        // compares false, while it has none)
+        float top[NH][2];
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                x[nh][j] = kf[nh][j] * fmaf(s00, sc[0][nh][j], fmaf(s01, sc[1][nh][j],
-                                            fmaf(c00, qs[0][nh][j], c01 * qs[1][nh][j])));
-                x[nh][2 + j] = kf[nh][j] * fmaf(s10, sc[0][nh][2 + j], fmaf(s11, sc[1][nh][2 + j],
-                                                fmaf(c10, qs[0][nh][j], c11 * qs[1][nh][j])));
+                top[nh][j] = fmaxf(x[0][nh][j], x[0][nh][2 + j]);
+                if (TT == 2) top[nh][j] = fmaxf(top[nh][j], fmaxf(x[TT - 1][nh][j], x[TT - 1][nh][2 + j]));
+                above = fmaxf(above, top[nh][j] - mh[nh][j]);
             }
-        if (partial) {
-#pragma unroll
-            for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (!ok0) x[nh][j] = -INFINITY;
-                    if (!ok1) x[nh][2 + j] = -INFINITY;
-                }
-        }
-        // (the difference is +inf for the first score of a head, NaN, which
-        // compares false, while it has none)
-#pragma unroll
-        for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) above = fmaxf(above, fmaxf(x[nh][j], x[nh][2 + j]) - mh[nh][j]);
-        if (__any_sync(~0u, above > kLazy || fmaxf(v00, v10) > smax[0] || fmaxf(v01, v11) > smax[1])) {
+        if (__any_sync(~0u, above > kLazy || vs[0] > smax[0] || vs[1] > smax[1])) {
             float re[2] = {1.f, 1.f};   // what the halves' sums are rescaled by
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                float m = half ? fmaxf(v01, v11) : fmaxf(v00, v10);
+                float m = vs[half];
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, off));
                 if (m > smax[half]) {
@@ -426,7 +438,7 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const
             for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float m = fmaxf(mh[nh][j], fmaxf(x[nh][j], x[nh][2 + j]));
+                    float m = fmaxf(mh[nh][j], top[nh][j]);
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, off));
                     const float al = m == -INFINITY ? 1.f : ex2(mh[nh][j] - m);   // 0 for a head that was empty
@@ -445,46 +457,51 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const
                 }
         }
         // ---- weights; P'^T (tokens x heads) per half as B fragments (k = tokens)
-        const float w00 = v00 * keep[0], w01 = v01 * keep[1], w10 = v10 * keep[0], w11 = v11 * keep[1];
-        const float z00 = fmaf(8.f, v00, bf_hi(p0.z)), z01 = fmaf(8.f, v01, bf_hi(p0.w));
-        const float z10 = fmaf(8.f, v10, bf_hi(p1.z)), z11 = fmaf(8.f, v11, bf_hi(p1.w));
-        uint32_t pb[2][NH][2];
+        uint32_t pb[TT][2][NH][2];
 #pragma unroll
-        for (int nh = 0; nh < NH; ++nh) {
-            float p[4];
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                p[j] = ex2(x[nh][j] - mz[nh][j]);
-                p[2 + j] = ex2(x[nh][2 + j] - mz[nh][j]);
-                lh[nh][j] += p[j] + p[2 + j];
-                zs[0][nh][j] = fmaf(p[j], z00, fmaf(p[2 + j], z10, zs[0][nh][j]));
-                zs[1][nh][j] = fmaf(p[j], z01, fmaf(p[2 + j], z11, zs[1][nh][j]));
+            for (int r = 0; r < 2; ++r) {
+                const uint4 &pr = par[t][r];
+                const float v0 = bf_lo(pr.z), v1 = bf_lo(pr.w);
+                const float w0 = v0 * keep[0], w1 = v1 * keep[1];
+                const float z0 = bf_hi(pr.z), z1 = bf_hi(pr.w);
+#pragma unroll
+                for (int nh = 0; nh < NH; ++nh) {
+                    float p[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        p[j] = ex2(x[t][nh][2 * r + j] - mz[nh][j]);
+                        lh[nh][j] += p[j];
+                        zs[0][nh][j] = fmaf(p[j], z0, zs[0][nh][j]);
+                        zs[1][nh][j] = fmaf(p[j], z1, zs[1][nh][j]);
+                    }
+                    pb[t][0][nh][r] = movm(pack_pair(p[0] * w0, p[1] * w0));
+                    pb[t][1][nh][r] = movm(pack_pair(p[0] * w1, p[1] * w1));
+                }
             }
-            pb[0][nh][0] = movm(pack_pair(p[0] * w00, p[1] * w00));
-            pb[0][nh][1] = movm(pack_pair(p[2] * w10, p[3] * w10));
-            pb[1][nh][0] = movm(pack_pair(p[0] * w01, p[1] * w01));
-            pb[1][nh][1] = movm(pack_pair(p[2] * w11, p[3] * w11));
-        }
         // ---- O^T += V^T P'^T: transposed 8x8 loads of the code bytes give, per
         // register, 4 channels of tokens 2tq (low half) and 2tq + 1 (high half)
 #pragma unroll
-        for (int c2 = 0; c2 < CB; c2 += 2) {
-            uint32_t w[4];
-            ldsm4_t(quad + Kv4<D>::V + c2 * 16, w);
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint32_t f0[4], f1[4];
-                widen(w[2 * u], f0);
-                widen(w[2 * u + 1], f1);
-                const int cb = c2 + u, half = cb / CBH;
+            for (int c2 = 0; c2 < CB; c2 += 2) {
+                uint32_t w[4];
+                ldsm4_t(quad0 + at + t * 16 * REC + Kv4<D>::V + c2 * 16, w);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t f0[4], f1[4];
+                    widen(w[2 * u], f0);
+                    widen(w[2 * u + 1], f1);
+                    const int cb = c2 + u, half = cb / CBH;
 #pragma unroll
-                    for (int nh = 0; nh < NH; ++nh)
-                        mma(o[cb][j][nh], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], pb[half][nh][0],
-                            pb[half][nh][1]);
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int nh = 0; nh < NH; ++nh)
+                            mma(o[cb][j][nh], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], pb[t][half][nh][0],
+                                pb[t][half][nh][1]);
+                }
             }
-        }
     };
     constexpr uint32_t kNone = 0xffffffffu;
     // ring step g: its mask is kept by lane g % kDST
@@ -508,8 +525,8 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const
             __syncwarp();   // every lane's copies of this stage are there
             const uint32_t mask = __shfl_sync(~0u, held, stage);
 #pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-                const uint32_t m = t ? mask >> 16 : mask & 0xffffu;
+            for (int t = 0; t < 2; t += TT) {
+                const uint32_t m = TT == 2 ? mask : t ? mask >> 16 : mask & 0xffffu;
                 if (m) consume(stage * SM::STAGE + t * 16 * REC, m);
             }
             __syncwarp();   // every lane is done with this stage before it is refilled
@@ -609,12 +626,19 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const
             const int na = min(max(la, 0), 16), nb = min(max(lb, 0), 16);
             const uint32_t dst = ring_a + stage * SM::STAGE + lane * 16;
             const uint8_t *pa = pool + (size_t)ra * REC + lane * 16, *pb = pool + (size_t)rb * REC + lane * 16 - 16 * REC;
-            const int ea = na * REC, eb = (16 + nb) * REC;
+            constexpr int COPIES = kDR * REC / 512;   // 512 bytes an instruction (REC is a multiple of 16)
+            if (na == 16 && nb == 16) {
 #pragma unroll
-            for (int c = 0; c < (kDR * REC + 511) / 512; ++c) {
-                const int at = c * 512 + lane * 16;
-                const bool second = at >= 16 * REC;
-                if (at < (second ? eb : ea)) copy16(dst + c * 512, (second ? pb : pa) + c * 512);
+                for (int c = 0; c < COPIES; ++c)
+                    copy16(dst + c * 512, (c * 512 + lane * 16 >= 16 * REC ? pb : pa) + c * 512);
+            } else {
+                const int ea = na * REC, eb = (16 + nb) * REC;
+#pragma unroll 1
+                for (int c = 0; c < COPIES; ++c) {
+                    const int at = c * 512 + lane * 16;
+                    const bool second = at >= 16 * REC;
+                    if (at < (second ? eb : ea)) copy16(dst + c * 512, (second ? pb : pa) + c * 512);
+                }
             }
             hold(stage, ((1u << na) - 1u) | (((1u << nb) - 1u) << 16));
         });
@@ -635,18 +659,24 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 4 : 2) k_decode_kv4(const
     float *mo = reinterpret_cast<float *>(sm);                 // [warp][16][D]
     float *mm = mo + kDW * 16 * D;                              // [warp][16]
     float *ml = mm + kDW * 16;                                  // [warp][16]
+    // (a token list has one head, column 0; for the others all columns are
+    // written, since a test of each costs more)
+    if (!TOKENS || tq == 0) {
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb)
+        for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int nh = 0; nh < NH; ++nh)
+                for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int h = nh * 8 + 2 * tq + (i & 1), half = cb / CBH;
-                    const int c = cb * 32 + 4 * gq + 2 * j + (i >> 1);
-                    mo[(warp * 16 + h) * D + c] =  fmaf(o[cb][j][nh][i], 1.f / keep[half], zs[half][nh][i & 1]);
-                }
+                    for (int i = 0; i < 4; i += TOKENS ? 2 : 1) {
+                        const int h = nh * 8 + 2 * tq + (i & 1), half = cb / CBH;
+                        const int c = cb * 32 + 4 * gq + 2 * j + (i >> 1);
+                        // (rows gq + 8 hold odd channels, whose codes went in as 16 c)
+                        mo[(warp * 16 + h) * D + c] = fmaf(o[cb][j][nh][i] * ((i >> 1) ? 1048576.f : 16777216.f),
+                                                           1.f / keep[half], zs[half][nh][i & 1]);
+                    }
+    }
     if (gq == 0) {
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh)
@@ -713,7 +743,7 @@ cudaError_t launch_kv4(const DecodeArgs &a, cudaStream_t s)
     auto kern = k_decode_kv4<D, NH, QF32, TOKENS>;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
     const int hpg = a.Hq / a.c.Hkv;
-    const dim3 grid((unsigned)a.S, (unsigned)(TOKENS ? a.Hq : a.c.Hkv * ((hpg + 15) / 16)), (unsigned)a.c.B);
+    const dim3 grid((unsigned)(TOKENS ? a.Hq : a.c.Hkv * ((hpg + 15) / 16)), (unsigned)a.c.B, (unsigned)a.S);
     return launch_pdl(kern, grid, dim3(kDThreads), smem, s, a);
 }
 
@@ -726,13 +756,16 @@ cudaError_t launch_kind(const DecodeArgs &a, cudaStream_t s)
 
 }  // namespace
 
-// Enough CTAs to fill the device about twice over (ragged lists even out), but
-// no split below 256 tokens of the longest possible list.
+// Enough CTAs to fill the device (3 an SM) between two and three times over,
+// but no split below 512 tokens of the longest possible list: at 32 x 8 groups
+// of up to 16384 tokens 3, 4, 5 and 8 splits take 105, 95, 94 and 99 us, at 32
+// x 32 lists of 4096 tokens 1, 2 and 3 take 167, 150 and 158 us, and at 4 x 8
+// lists of up to 4096 tokens (one wave of CTAs) 4, 8 and 16 take 17, 12 and 13.
 int decode_kv4_splits(int B, int rows, long long list)
 {
     const long long units = (long long)B * rows;
     if (units <= 0) return 1;
-    const long long want = (2 * 148 * 4 + units - 1) / units, most = (list + 255) / 256;
+    const long long want = (2 * 148 * 4 + units - 1) / units, most = (list + 511) / 512;
     const long long s = want < most ? want : most;
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
