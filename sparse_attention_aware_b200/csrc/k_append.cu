@@ -12,18 +12,23 @@
 // each half of a row, zero = bf16(min), scale = bf16((max - min) / 15) (each
 // through fp32) and codes rint((y - zero) / scale), ties to even, clamped to
 // [0, 15]; a half that holds a value that is not finite is stored with scale
-// and zero NaN.  Keys and values for 4-bit pages are computed in fp64 up to
-// the codes: an fp32 norm is a few ulps off, which next to a border between
-// two codes stores another code, a full step away.  With fp64 the stored
-// bytes are those of the definition, whatever the call's shape.
+// and zero NaN.  The stored bytes are those of the definition in fp64, whatever
+// the call's shape: rows are computed in fp32 with a bound on their error, and a
+// warp one of whose rows has a code, scale or zero nearer to a border than that
+// (about one in twenty) computes it again in fp64.  (A code next to a border
+// would otherwise come out a full step off; all of it in fp64 took 258 us for
+// 16391 tokens of 32 + 2 x 8 heads.)
 //
 // Angles are formed in fp64 (position * inv_freq is exact below 2^29),
 // reduced by 2 pi in two parts (Cody and Waite) and only then rounded for the
 // fp32 sine: fp32 angles of positions near 2^20 would be off by up to 0.06.
 //
-// One CTA per token (and slice of its heads); a warp takes 32 / (D/8) heads of
-// one kind, 8 channels a lane.  Bound by HBM for prompts (rows in, rows out),
-// by latency for single steps.
+// A warp takes a token's heads (or a slice of them, when there are few tokens)
+// 32 / (D/8) at a time, kBatch rows a lane in flight; its lanes share out the
+// token's angles.  A lane holds two runs of 4 channels whose elements turn with
+// one another (4g.. and rot/2 + 4g.., or 8g.. and 8g + 4.. where pairs are
+// neighbours), so the rotation needs no exchange between lanes.  Bound by HBM
+// for prompts (rows in, rows out), by latency for single steps.
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"
@@ -46,19 +51,20 @@ __device__ __forceinline__ double reduce_2pi(double x)
     return fma(-k, 2.4492935982947064e-16, r);
 }
 
+__device__ __forceinline__ float inv_root(float x) { return rsqrtf(x); }   // within 2 ulps
+__device__ __forceinline__ double inv_root(double x) { return 1.0 / sqrt(x); }
+
 template <int D, typename F>
-__device__ __forceinline__ void norm_row(F (&x)[8], const F (&w)[8], bool has_w, float eps)
+__device__ __forceinline__ void norm_row(F (&x)[8], const F (&w)[8], float eps)
 {
     F ss = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fma(x[e], x[e], ss);
 #pragma unroll
     for (int o = D / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-    if (has_w) {
-        const F r = (F)1 / sqrt(ss / (F)D + (F)eps);
+    const F r = inv_root(ss * (F)(1.0 / D) + (F)eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
-    }
+    for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
 }
 
 // cs: the lane's 8 angles (pairs apart: angle of channel e; pairs together:
@@ -97,6 +103,18 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+__device__ __forceinline__ void load_weight(const void *w, bool f32, int e0, float (&wf)[8])
+{
+    if (f32) {
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(w) + e0);
+        const float4 x = p[0], y = p[1];
+        wf[0] = x.x; wf[1] = x.y; wf[2] = x.z; wf[3] = x.w;
+        wf[4] = y.x; wf[5] = y.y; wf[6] = y.z; wf[7] = y.w;
+    } else {
+        unpack8(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + e0), wf);
+    }
 }
 
 // One row (16 or 8 lanes, 8 channels each) to 4 bits: the lane's code word,
@@ -142,105 +160,289 @@ __device__ __forceinline__ void quantize_row(const double (&y)[8], uint32_t &cod
     }
 }
 
+// Codes (low word) and parameters of one kind of row (1: key, 2: value), in
+// fp64 from the start.  Called by whole warps; src null: no row.
+template <int D>
+__device__ __noinline__ uint2 append_row64(const AppendArgs &a, const uint16_t *src, int kind, long long t)
+{
+    const int e0 = (threadIdx.x & (D / 8 - 1)) * 8;
+    float x[8];
+    unpack8(src ? *reinterpret_cast<const uint4 *>(src + e0) : make_uint4(0, 0, 0, 0), x);
+    double y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = x[e];
+    if (kind == 1) {
+        if (a.k_weight) {
+            float wf[8];
+            load_weight(a.k_weight, a.w_f32, e0, wf);
+            double w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = wf[e];
+            norm_row<D>(y, w, a.eps);
+        }
+        const int n = a.rot / 2;
+        if (n > 0) {
+            Angle<double> cs[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                cs[e] = {1.0, 0.0};
+                if (e0 < a.rot) {
+                    const int i = a.interleaved ? e0 / 2 + (e & 3) : e0 < n ? e0 + e : e0 - n + e;
+                    sincos(reduce_2pi((double)a.pos[t] * (double)a.inv_freq[i]), &cs[e].sin, &cs[e].cos);
+                }
+            }
+            rope_row<D>(y, cs, e0, a.rot, a.interleaved);
+        }
+    }
+    uint2 r;
+    quantize_row<D>(y, r.x, r.y);
+    return r;
+}
+
+// The same from fp32 rows whose elements are off by at most 2^-18 of the row's
+// largest (exact: not at all).  Returns false in the lanes that see a border too
+// near.
+//
+// The bound, u = 2^-24: the norm's sum of squares is off by 13 u, its inverse
+// root by half of that and 4 u, each product by u: 13 u in all; sine and cosine
+// of a rounded angle by 2^-22 absolutely; with |a|, |b| up to sqrt(2) times the
+// largest element, a cos - b sin by 2 sqrt(2) (15 u + 2^-22) + u < 2^-18.
+template <int D>
+__device__ __forceinline__ bool quantize_row32(const float (&y)[8], bool exact, uint32_t &codes, uint32_t &par)
+{
+    constexpr int HL = D / 16;   // lanes of a half
+    float lo = y[0], hi = y[0], least = INFINITY;   // least: magnitude of the smallest element that is not 0
+    bool fine = true;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        lo = fminf(lo, y[e]);
+        hi = fmaxf(hi, y[e]);
+        fine = fine && isfinite(y[e]);
+        if (y[e] != 0.f) least = fminf(least, fabsf(y[e]));
+    }
+#pragma unroll
+    for (int o = HL / 2; o > 0; o >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
+    }
+    float top = fmaxf(fabsf(lo), fabsf(hi));
+    const float err = exact ? 0.f : fmaxf(top, __shfl_xor_sync(~0u, top, HL)) * 3.8146973e-6f;   // 2^-18, of the row
+    const unsigned half_lanes = ((1u << HL) - 1) << ((threadIdx.x & 31) & ~(HL - 1));
+    const unsigned finite = __ballot_sync(~0u, fine);
+    auto bf = [](float x) { return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x)); };
+    const float range = (hi - lo) * (1.f / 15.f), slack = fmaf(range, 4.8e-7f, 0.25f * err);   // 8 u, and 2 err / 15
+    const uint32_t zb = bf(lo - err), sb = bf(range - slack);
+    bool sure = zb == bf(lo + err) && sb == bf(range + slack) && (finite & half_lanes) == half_lanes;
+    const float z = bf_lo(zb), s = bf_lo(sb);
+    // subnormal or huge rows are left to fp64
+    sure = sure && s > 1e-30f && top < 1e30f;
+    const float inv = 1.f / s, near = 0.5f - fmaf(err, 1.01f * inv, 4e-6f);
+    if (exact) sure = sure && least > top * 3.0517578e-5f;   // 2^-15: then y - z is exact
+    codes = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float d = y[e] - z, c = rintf(d * inv);
+        float code = c;
+        if (exact) {
+            // the quotient is within 3 u: the nearest whole number, or a border; the
+            // sign of the distance from the border is exact in one fma
+            const float f = floorf(d * inv), over = fmaf(-(f + 0.5f), s, d);
+            code = over > 0.f || (over == 0.f && ((int)f & 1)) ? f + 1.f : f;
+        } else {
+            sure = sure && fabsf(fmaf(d, inv, -c)) < near;
+        }
+        codes |= (uint32_t)min(max((int)code, 0), 15) << (4 * e);
+    }
+    par = sb | (zb << 16);
+    return sure;
+}
+
+// A row (8 channels a lane, in order) into its record; src null: none.
+template <int D>
+__device__ __forceinline__ void store4(const AppendArgs &a, const float (&y)[8], bool exact, int kind, long long t,
+                                       const uint16_t *src, uint8_t *rec)
+{
+    const int gl = threadIdx.x & (D / 8 - 1);
+    uint32_t codes, par;
+    const bool sure = quantize_row32<D>(y, exact, codes, par);
+    if (!__all_sync(~0u, sure || !src)) {
+        const uint2 r = append_row64<D>(a, src, kind, t);
+        codes = r.x;
+        par = r.y;
+    }
+    if (src) {
+        *reinterpret_cast<uint32_t *>(rec + (kind == 2 ? Kv4<D>::V : 0) + gl * 4) = codes;
+        if ((gl & (D / 16 - 1)) == 0)
+            *reinterpret_cast<uint32_t *>(rec + Kv4<D>::PAR + (kind == 2 ? 8 : 0) + (gl ? 4 : 0)) = par;
+    }
+}
+
+constexpr int kBatch = 4;   // rows a lane has in flight
+
+// wpt warps share a token's heads
 template <int D, int BITS>
-__global__ void __launch_bounds__(kAppendThreads) k_rope_append(const AppendArgs a)
+__global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_append(const AppendArgs a, int wpt)
 {
     pdl_wait();
     pdl_trigger();
     constexpr int LPR = D / 8, RPW = 32 / LPR, WARPS = kAppendThreads / 32;
-    __shared__ Angle<double> s_ang[D / 2];
-    const long long t = blockIdx.x;
+    __shared__ Angle<float> s_ang[WARPS][D / 2];
+    __shared__ float4 s_row[BITS == 4 ? WARPS : 1][32 * 2];   // keys on their way to 4 bits: RPW rows
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long unit = (long long)blockIdx.x * WARPS + warp;
+    const long long t = unit / wpt;
+    const int first = (int)(unit - t * wpt);
+    if (t >= a.T) return;
     const int gl = lane & (LPR - 1), sub = lane / LPR, e0 = gl * 8;
     const int qt = (a.Hq + RPW - 1) / RPW, kt = (a.Hkv + RPW - 1) / RPW;
-    const int tasks = qt + 2 * kt;
-
     const int n = a.rot / 2;
-    if ((int)threadIdx.x < n) {
-        double s, c;
-        sincos(reduce_2pi((double)a.pos[t] * (double)a.inv_freq[threadIdx.x]), &s, &c);
-        s_ang[threadIdx.x] = {c, s};
-    }
+    // the lane's two runs of channels, and whether they turn with each other
+    const bool turns = gl < a.rot / 8, apart = turns && !a.interleaved;
+    const int ca = apart ? 4 * gl : e0, cb = apart ? n + 4 * gl : e0 + 4;
+
     const long long slot = a.slots[t];
     bool store = slot >= 0;
     if (slot < -1 || slot >= a.num_slots) {
-        if (threadIdx.x == 0 && blockIdx.y == 0) fault(a.st, CHK_SLOT, (int)slot);
+        if (lane == 0 && first == 0) fault(a.st, CHK_SLOT, (int)slot);
         store = false;
     }
-    __syncthreads();
-    Angle<float> cs[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        // pairs apart: channel e0 + e and its partner share angle (e0 + e) mod n
-        const int i = a.interleaved ? e0 / 2 + (e & 3) : e0 < n ? e0 + e : e0 - n + e;
-        const Angle<double> x = e0 < a.rot ? s_ang[i] : Angle<double>{1.0, 0.0};
-        cs[e] = {(float)x.cos, (float)x.sin};
-    }
-    const int off = (int)(slot & ((1 << a.Plog2) - 1));
-    const long long page = slot >> a.Plog2;
+    const size_t row0 = (((size_t)(slot >> a.Plog2) * a.Hkv) << a.Plog2) + (size_t)(slot & ((1 << a.Plog2) - 1));
 
-    for (int task = blockIdx.y * WARPS + warp; task < tasks; task += gridDim.y * WARPS) {
-        const int kind = task < qt ? 0 : task < qt + kt ? 1 : 2;
-        const int head = (task - (kind == 0 ? 0 : kind == 1 ? qt : qt + kt)) * RPW + sub;
-        const bool act = head < (kind == 0 ? a.Hq : a.Hkv);
-        if (kind != 0 && !store) continue;
-        const uint16_t *src = kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (act) raw = *reinterpret_cast<const uint4 *>(src + (size_t)head * D + e0);
-        const void *w = kind == 0 ? a.q_weight : a.k_weight;
-        const bool normed = kind != 2 && w != nullptr;
-        float wf[8];
-        if (normed) {
-            if (a.w_f32) {
-                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(w) + e0);
-                const float4 x = p[0], y = p[1];
-                wf[0] = x.x; wf[1] = x.y; wf[2] = x.z; wf[3] = x.w;
-                wf[4] = y.x; wf[5] = y.y; wf[6] = y.z; wf[7] = y.w;
-            } else {
-                unpack8(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + e0), wf);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) wf[e] = 1.f;
+    // the token's angles, shared out over the lanes
+    Angle<float> cs[4] = {{1.f, 0.f}, {1.f, 0.f}, {1.f, 0.f}, {1.f, 0.f}};
+    if (first < qt + kt && n > 0) {
+        const double pos = a.pos[t];
+        for (int i = lane; i < n; i += 32) {
+            Angle<float> x;
+            sincosf((float)reduce_2pi(pos * (double)a.inv_freq[i]), &x.sin, &x.cos);
+            s_ang[warp][i] = x;
         }
-        float x[8];
-        unpack8(raw, x);
-        const size_t row = (((size_t)page * a.Hkv + head) << a.Plog2) + off;   // of the cache, for keys and values
-        if (BITS == 4 && kind != 0) {
-            double y[8], w8[8];
+        __syncwarp();
+        if (turns) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e], w8[e] = wf[e];
-            if (kind == 1) {
-                norm_row<D>(y, w8, normed, a.eps);
-                if (n > 0) {
-                    Angle<double> c8[8];
+            for (int e = 0; e < 4; ++e) cs[e] = s_ang[warp][4 * gl + e];
+        }
+    }
+
+    // norm and rotation of a row: x[0..3] at channel ca, x[4..7] at cb
+    auto turn = [&](float (&x)[8], const void *w, const float (&wf)[8]) {
+        if (w) norm_row<D>(x, wf, a.eps);
+        if (a.interleaved) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int i = a.interleaved ? e0 / 2 + (e & 3) : e0 < n ? e0 + e : e0 - n + e;
-                        c8[e] = e0 < a.rot ? s_ang[i] : Angle<double>{1.0, 0.0};
-                    }
-                    rope_row<D>(y, c8, e0, a.rot, a.interleaved);
+            for (int p = 0; p < 4; ++p) {
+                const float u = x[2 * p], v = x[2 * p + 1];
+                if (turns) {
+                    x[2 * p] = fmaf(u, cs[p].cos, -v * cs[p].sin);
+                    x[2 * p + 1] = fmaf(v, cs[p].cos, u * cs[p].sin);
                 }
             }
-            uint32_t codes, par;
-            quantize_row<D>(y, codes, par);
-            if (act) {
-                uint8_t *rec = a.kv4 + row * Kv4<D>::REC;
-                *reinterpret_cast<uint32_t *>(rec + (kind == 2 ? Kv4<D>::V : 0) + gl * 4) = codes;
-                if ((gl & (LPR / 2 - 1)) == 0)
-                    *reinterpret_cast<uint32_t *>(rec + Kv4<D>::PAR + (kind == 2 ? 8 : 0) + (gl ? 4 : 0)) = par;
+        } else if (turns) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float u = x[p], v = x[4 + p];
+                x[p] = fmaf(u, cs[p].cos, -v * cs[p].sin);
+                x[4 + p] = fmaf(v, cs[p].cos, u * cs[p].sin);
             }
-            continue;
         }
-        if (kind != 2) {
-            norm_row<D>(x, wf, normed, a.eps);
-            if (n > 0) rope_row<D>(x, cs, e0, a.rot, a.interleaved);
-            raw = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+    };
+    // this warp's tasks of a kind whose tasks begin at `from` of all of them
+    auto start = [&](int from) { return wpt == 1 ? 0 : (first + wpt - from % wpt) % wpt; };
+    // heads of a kind, kBatch rows at a time: row(head, channels ca and cb)
+    auto rows = [&](const uint16_t *src, int heads, int tasks, int begin, auto &&row) {
+        const uint16_t *pa = src + sub * D + ca, *pb = src + sub * D + cb;
+        for (int i = begin; i < tasks; i += kBatch * wpt) {
+            uint2 ra[kBatch], rb[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int head = (i + u * wpt) * RPW;
+                ra[u] = rb[u] = make_uint2(0, 0);
+                if (head + sub < heads) {
+                    ra[u] = *reinterpret_cast<const uint2 *>(pa + (size_t)head * D);
+                    rb[u] = *reinterpret_cast<const uint2 *>(pb + (size_t)head * D);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int head = (i + u * wpt) * RPW;
+                if (head >= heads) break;
+                float x[8];
+                unpack8(make_uint4(ra[u].x, ra[u].y, rb[u].x, rb[u].y), x);
+                row(head + sub, head + sub < heads, x);
+            }
         }
-        if (act) {
-            uint16_t *dst = kind == 0 ? a.q_out + t * a.q_out_stride + (size_t)head * D
-                                      : (kind == 1 ? a.kp : a.vp) + row * D;
-            *reinterpret_cast<uint4 *>(dst + e0) = raw;
+    };
+    auto put = [&](uint16_t *dst, const float (&x)[8]) {
+        *reinterpret_cast<uint2 *>(dst + ca) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+        *reinterpret_cast<uint2 *>(dst + cb) = make_uint2(pack2(x[4], x[5]), pack2(x[6], x[7]));
+    };
+    float wf[8];
+    auto weight = [&](const void *w) {
+        float half[8];
+        load_weight(w, a.w_f32, ca & ~7, half);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wf[e] = (ca & 4) ? half[4 + e] : half[e];
+        load_weight(w, a.w_f32, cb & ~7, half);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wf[4 + e] = (cb & 4) ? half[4 + e] : half[e];
+    };
+
+    // ---- queries
+    const int q0 = start(0);
+    if (q0 < qt) {
+        if (a.q_weight) weight(a.q_weight);
+        uint16_t *out = a.q_out + t * a.q_out_stride;
+        rows(a.q + t * a.q_stride, a.Hq, qt, q0, [&](int head, bool act, float (&x)[8]) {
+            turn(x, a.q_weight, wf);
+            if (act) put(out + (size_t)head * D, x);
+        });
+    }
+    if (!store) return;
+    // ---- keys
+    const uint16_t *kp = a.k + t * a.k_stride, *vp = a.v + t * a.v_stride;
+    const int k0 = start(qt);
+    if (k0 < kt) {
+        if (a.k_weight) weight(a.k_weight);
+        rows(kp, a.Hkv, kt, k0, [&](int head, bool act, float (&x)[8]) {
+            turn(x, a.k_weight, wf);
+            const size_t at = row0 + ((size_t)head << a.Plog2);
+            if (BITS == 16) {
+                if (act) put(a.kp + at * D, x);
+            } else {
+                // back to 8 channels a lane, in order
+                float *r = reinterpret_cast<float *>(s_row[warp]) + sub * D;
+                __syncwarp();
+                *reinterpret_cast<float4 *>(r + ca) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4 *>(r + cb) = make_float4(x[4], x[5], x[6], x[7]);
+                __syncwarp();
+                const float4 u = *reinterpret_cast<const float4 *>(r + e0), v = *reinterpret_cast<const float4 *>(r + e0 + 4);
+                const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+                store4<D>(a, y, !a.k_weight && n == 0, 1, t, act ? kp + (size_t)head * D : nullptr,
+                          a.kv4 + at * Kv4<D>::REC);
+            }
+        });
+    }
+    // ---- values, 8 channels a lane in order
+    const int v0 = start(qt + kt);
+    for (int i = v0; i < kt; i += kBatch * wpt) {
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int head = (i + u * wpt) * RPW + sub;
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (head < a.Hkv) raw[u] = *reinterpret_cast<const uint4 *>(vp + (size_t)head * D + e0);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int head = (i + u * wpt) * RPW + sub;
+            if (head - sub >= a.Hkv) break;
+            const size_t at = row0 + ((size_t)head << a.Plog2);
+            if (BITS == 16) {
+                if (head < a.Hkv) *reinterpret_cast<uint4 *>(a.vp + at * D + e0) = raw[u];
+            } else {
+                float x[8];
+                unpack8(raw[u], x);
+                store4<D>(a, x, true, 2, t, head < a.Hkv ? vp + (size_t)head * D : nullptr, a.kv4 + at * Kv4<D>::REC);
+            }
         }
     }
 }
@@ -250,19 +452,17 @@ __global__ void __launch_bounds__(kAppendThreads) k_rope_append(const AppendArgs
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s)
 {
     if (a.T == 0) return cudaSuccess;
-    const int rpw = 256 / a.D, warps = kAppendThreads / 32;
+    const int rpw = 256 / a.D;
     const int tasks = (a.Hq + rpw - 1) / rpw + 2 * ((a.Hkv + rpw - 1) / rpw);
-    // few tokens: spread a token's heads over CTAs, so that a step is not a
-    // serial walk over its heads
-    const int most = (tasks + warps - 1) / warps;
-    const int slices = a.T >= 296 ? 1 : most;
-    const dim3 grid((unsigned)a.T, (unsigned)slices);
-    if (a.kv4) {
-        if (a.D == 64) return launch_pdl(k_rope_append<64, 4>, grid, dim3(kAppendThreads), 0, s, a);
-        return launch_pdl(k_rope_append<128, 4>, grid, dim3(kAppendThreads), 0, s, a);
-    }
-    if (a.D == 64) return launch_pdl(k_rope_append<64, 16>, grid, dim3(kAppendThreads), 0, s, a);
-    return launch_pdl(k_rope_append<128, 16>, grid, dim3(kAppendThreads), 0, s, a);
+    // a warp per token, or more while that leaves the device short of warps
+    // (32 an SM, twice): one token's heads are then taken at once
+    long long wpt = (2 * 148 * 32 + a.T - 1) / a.T;
+    wpt = wpt < 1 ? 1 : wpt > tasks ? tasks : wpt;
+    const long long warps = wpt * a.T;
+    const dim3 grid((unsigned)((warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32)));
+    auto kern = a.kv4 ? (a.D == 64 ? k_rope_append<64, 4> : k_rope_append<128, 4>)
+                      : (a.D == 64 ? k_rope_append<64, 16> : k_rope_append<128, 16>);
+    return launch_pdl(kern, grid, dim3(kAppendThreads), 0, s, a, (int)wpt);
 }
 
 }  // namespace sa
