@@ -200,81 +200,82 @@ __device__ __noinline__ uint2 append_row64(const AppendArgs &a, const uint16_t *
 }
 
 // The same from fp32 rows whose elements are off by at most 2^-18 of the row's
-// largest (exact: not at all).  Returns false in the lanes that see a border too
+// largest (EXACT: not at all).  Returns false in the lanes that see a border too
 // near.
 //
 // The bound, u = 2^-24: the norm's sum of squares is off by 13 u, its inverse
 // root by half of that and 4 u, each product by u: 13 u in all; sine and cosine
 // of a rounded angle by 2^-22 absolutely; with |a|, |b| up to sqrt(2) times the
 // largest element, a cos - b sin by 2 sqrt(2) (15 u + 2^-22) + u < 2^-18.
-template <int D>
-__device__ __forceinline__ bool quantize_row32(const float (&y)[8], bool exact, uint32_t &codes, uint32_t &par)
+template <int D, bool EXACT>
+__device__ __forceinline__ bool quantize_row32(const float (&y)[8], uint32_t &codes, uint32_t &par)
 {
-    constexpr int HL = D / 16;   // lanes of a half
-    float lo = y[0], hi = y[0], least = INFINITY;   // least: magnitude of the smallest element that is not 0
-    bool fine = true;
+    constexpr int HL = D / 16;               // lanes of a half
+    constexpr float MAGIC = 12582912.f;      // 1.5 * 2^23: x + MAGIC holds the nearest whole number in its low bits
+    float lo = y[0], hi = y[0], nan = 0.f;   // nan: not a number if an element is not finite
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         lo = fminf(lo, y[e]);
         hi = fmaxf(hi, y[e]);
-        fine = fine && isfinite(y[e]);
-        if (y[e] != 0.f) least = fminf(least, fabsf(y[e]));
+        nan = fmaf(y[e], 0.f, nan);
     }
 #pragma unroll
     for (int o = HL / 2; o > 0; o >>= 1) {
         lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
     }
-    float top = fmaxf(fabsf(lo), fabsf(hi));
-    const float err = exact ? 0.f : fmaxf(top, __shfl_xor_sync(~0u, top, HL)) * 3.8146973e-6f;   // 2^-18, of the row
     const unsigned half_lanes = ((1u << HL) - 1) << ((threadIdx.x & 31) & ~(HL - 1));
-    const unsigned finite = __ballot_sync(~0u, fine);
+    const unsigned finite = __ballot_sync(~0u, nan == 0.f);
+    const float top = fmaxf(fabsf(lo), fabsf(hi));
+    const float err = EXACT ? 0.f : fmaxf(top, __shfl_xor_sync(~0u, top, HL)) * 3.8146973e-6f;   // 2^-18, of the row
     auto bf = [](float x) { return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x)); };
     const float range = (hi - lo) * (1.f / 15.f), slack = fmaf(range, 4.8e-7f, 0.25f * err);   // 8 u, and 2 err / 15
     const uint32_t zb = bf(lo - err), sb = bf(range - slack);
-    bool sure = zb == bf(lo + err) && sb == bf(range + slack) && (finite & half_lanes) == half_lanes;
     const float z = bf_lo(zb), s = bf_lo(sb);
-    // subnormal or huge rows are left to fp64
-    sure = sure && s > 1e-30f && top < 1e30f;
-    const float inv = 1.f / s, near = 0.5f - fmaf(err, 1.01f * inv, 4e-6f);
-    if (exact) sure = sure && least > top * 3.0517578e-5f;   // 2^-15: then y - z is exact
-    codes = 0;
+    // (subnormal or huge rows are left to fp64)
+    bool sure = zb == bf(lo + err) && sb == bf(range + slack) && (finite & half_lanes) == half_lanes && s > 1e-30f &&
+                top < 1e30f;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));   // within 1 ulp
+    // quotients y / s - z / s: each product and the quotient's reciprocal are within 4 u
+    const float zi = z * inv, near = 0.5f - fmaf(err, 1.01f * inv, fmaf((fabsf(z) + top) * inv, 4.8e-7f, 4e-6f));
+    float far = 0.f;
+    codes = 0u;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float d = y[e] - z, c = rintf(d * inv);
-        float code = c;
-        if (exact) {
-            // the quotient is within 3 u: the nearest whole number, or a border; the
-            // sign of the distance from the border is exact in one fma
-            const float f = floorf(d * inv), over = fmaf(-(f + 0.5f), s, d);
-            code = over > 0.f || (over == 0.f && ((int)f & 1)) ? f + 1.f : f;
-        } else {
-            sure = sure && fabsf(fmaf(d, inv, -c)) < near;
-        }
-        codes |= (uint32_t)min(max((int)code, 0), 15) << (4 * e);
+        const float t = fmaf(y[e], inv, -zi), m = t + MAGIC;
+        far = fmaxf(far, fabsf(t - (m - MAGIC)));
+        codes += __float_as_uint(fminf(fmaxf(m, MAGIC), MAGIC + 15.f)) * (1u << (4 * e));
     }
+    codes -= 0x4b400000u * 0x11111111u;   // MAGIC's own bits
     par = sb | (zb << 16);
+    if (EXACT) {
+        // elements on a border are common (bf16 numbers): the sign of the distance
+        // from a border is exact in one fma if y - z is
+        if (__any_sync(~0u, !(far < near))) {
+            codes = 0u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = y[e] - z, f = floorf(d * inv), over = fmaf(-(f + 0.5f), s, d);
+                sure = sure && d + z == y[e] && y[e] - d == z;
+                const int c = (int)f + (over > 0.f || (over == 0.f && ((int)f & 1)));
+                codes |= (uint32_t)min(max(c, 0), 15) << (4 * e);
+            }
+        }
+    } else {
+        sure = sure && far < near;
+    }
     return sure;
 }
 
-// A row (8 channels a lane, in order) into its record; src null: none.
+// A row's code word and its half's parameters into its record
 template <int D>
-__device__ __forceinline__ void store4(const AppendArgs &a, const float (&y)[8], bool exact, int kind, long long t,
-                                       const uint16_t *src, uint8_t *rec)
+__device__ __forceinline__ void put4(uint8_t *rec, int kind, uint32_t codes, uint32_t par)
 {
     const int gl = threadIdx.x & (D / 8 - 1);
-    uint32_t codes, par;
-    const bool sure = quantize_row32<D>(y, exact, codes, par);
-    if (!__all_sync(~0u, sure || !src)) {
-        const uint2 r = append_row64<D>(a, src, kind, t);
-        codes = r.x;
-        par = r.y;
-    }
-    if (src) {
-        *reinterpret_cast<uint32_t *>(rec + (kind == 2 ? Kv4<D>::V : 0) + gl * 4) = codes;
-        if ((gl & (D / 16 - 1)) == 0)
-            *reinterpret_cast<uint32_t *>(rec + Kv4<D>::PAR + (kind == 2 ? 8 : 0) + (gl ? 4 : 0)) = par;
-    }
+    *reinterpret_cast<uint32_t *>(rec + (kind == 2 ? Kv4<D>::V : 0) + gl * 4) = codes;
+    if ((gl & (D / 16 - 1)) == 0)
+        *reinterpret_cast<uint32_t *>(rec + Kv4<D>::PAR + (kind == 2 ? 8 : 0) + (gl ? 4 : 0)) = par;
 }
 
 constexpr int kBatch = 4;   // rows a lane has in flight
@@ -347,8 +348,14 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_appe
     };
     // this warp's tasks of a kind whose tasks begin at `from` of all of them
     auto start = [&](int from) { return wpt == 1 ? 0 : (first + wpt - from % wpt) % wpt; };
-    // heads of a kind, kBatch rows at a time: row(head, channels ca and cb)
-    auto rows = [&](const uint16_t *src, int heads, int tasks, int begin, auto &&row) {
+    // tasks of this warp to be done again in fp64 (4 bits): of keys, of values.
+    // They wait for the end: a call between the rows would have the rows' state
+    // moved to memory around it
+    uint32_t redo[2] = {0u, 0u};
+    // heads of a kind, kBatch rows at a time: row(head, channels ca and cb) says
+    // whether it was sure
+    auto rows = [&](const uint16_t *src, int heads, int tasks, int begin, uint32_t *unsure, auto &&row) {
+        uint32_t bit = 1u;
         const uint16_t *pa = src + sub * D + ca, *pb = src + sub * D + cb;
         for (int i = begin; i < tasks; i += kBatch * wpt) {
             uint2 ra[kBatch], rb[kBatch];
@@ -367,7 +374,9 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_appe
                 if (head >= heads) break;
                 float x[8];
                 unpack8(make_uint4(ra[u].x, ra[u].y, rb[u].x, rb[u].y), x);
-                row(head + sub, head + sub < heads, x);
+                const bool act = head + sub < heads, sure = row(head + sub, act, x);
+                if (unsure && !__all_sync(~0u, sure || !act)) *unsure |= bit;
+                bit <<= 1;
             }
         }
     };
@@ -391,22 +400,25 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_appe
     if (q0 < qt) {
         if (a.q_weight) weight(a.q_weight);
         uint16_t *out = a.q_out + t * a.q_out_stride;
-        rows(a.q + t * a.q_stride, a.Hq, qt, q0, [&](int head, bool act, float (&x)[8]) {
+        rows(a.q + t * a.q_stride, a.Hq, qt, q0, nullptr, [&](int head, bool act, float (&x)[8]) {
             turn(x, a.q_weight, wf);
             if (act) put(out + (size_t)head * D, x);
+            return true;
         });
     }
     if (!store) return;
+    const bool plain = !a.k_weight && n == 0;   // keys as they came
     // ---- keys
     const uint16_t *kp = a.k + t * a.k_stride, *vp = a.v + t * a.v_stride;
     const int k0 = start(qt);
     if (k0 < kt) {
         if (a.k_weight) weight(a.k_weight);
-        rows(kp, a.Hkv, kt, k0, [&](int head, bool act, float (&x)[8]) {
+        rows(kp, a.Hkv, kt, k0, BITS == 4 ? &redo[0] : nullptr, [&](int head, bool act, float (&x)[8]) {
             turn(x, a.k_weight, wf);
             const size_t at = row0 + ((size_t)head << a.Plog2);
             if (BITS == 16) {
                 if (act) put(a.kp + at * D, x);
+                return true;
             } else {
                 // back to 8 channels a lane, in order
                 float *r = reinterpret_cast<float *>(s_row[warp]) + sub * D;
@@ -416,13 +428,16 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_appe
                 __syncwarp();
                 const float4 u = *reinterpret_cast<const float4 *>(r + e0), v = *reinterpret_cast<const float4 *>(r + e0 + 4);
                 const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-                store4<D>(a, y, !a.k_weight && n == 0, 1, t, act ? kp + (size_t)head * D : nullptr,
-                          a.kv4 + at * Kv4<D>::REC);
+                uint32_t codes, par;
+                const bool sure = plain ? quantize_row32<D, true>(y, codes, par) : quantize_row32<D, false>(y, codes, par);
+                if (act) put4<D>(a.kv4 + at * Kv4<D>::REC, 1, codes, par);
+                return sure;
             }
         });
     }
     // ---- values, 8 channels a lane in order
     const int v0 = start(qt + kt);
+    uint32_t bit = 1u;
     for (int i = v0; i < kt; i += kBatch * wpt) {
         uint4 raw[kBatch];
 #pragma unroll
@@ -441,7 +456,22 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_appe
             } else {
                 float x[8];
                 unpack8(raw[u], x);
-                store4<D>(a, x, true, 2, t, head < a.Hkv ? vp + (size_t)head * D : nullptr, a.kv4 + at * Kv4<D>::REC);
+                uint32_t codes, par;
+                const bool act = head < a.Hkv, sure = quantize_row32<D, true>(x, codes, par);
+                if (act) put4<D>(a.kv4 + at * Kv4<D>::REC, 2, codes, par);
+                if (!__all_sync(~0u, sure || !act)) redo[1] |= bit;
+                bit <<= 1;
+            }
+        }
+    }
+    if (BITS == 4) {
+        for (int kind = 1; kind <= 2; ++kind) {
+#pragma unroll 1
+            for (uint32_t m = kind == 1 ? redo[0] : redo[1]; m; m &= m - 1) {
+                const int head = ((kind == 1 ? k0 : v0) + (__ffs(m) - 1) * wpt) * RPW + sub;
+                const bool act = head < a.Hkv;
+                const uint2 r = append_row64<D>(a, act ? (kind == 1 ? kp : vp) + (size_t)head * D : nullptr, kind, t);
+                if (act) put4<D>(a.kv4 + (row0 + ((size_t)head << a.Plog2)) * Kv4<D>::REC, kind, r.x, r.y);
             }
         }
     }
@@ -457,7 +487,9 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t s)
     // a warp per token, or more while that leaves the device short of warps
     // (32 an SM, twice): one token's heads are then taken at once
     long long wpt = (2 * 148 * 32 + a.T - 1) / a.T;
-    wpt = wpt < 1 ? 1 : wpt > tasks ? tasks : wpt;
+    // (a warp keeps marks of up to 32 tasks of a kind)
+    const int least = (a.Hkv + 32 * rpw - 1) / (32 * rpw);
+    wpt = wpt < least ? least : wpt > tasks ? tasks : wpt;
     const long long warps = wpt * a.T;
     const dim3 grid((unsigned)((warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32)));
     auto kern = a.kv4 ? (a.D == 64 ? k_rope_append<64, 4> : k_rope_append<128, 4>)
