@@ -127,14 +127,15 @@ __device__ __forceinline__ void quantize_row(const double (&y)[8], uint32_t &cod
     bool fine = true;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        lo = fmin(lo, y[e]);
-        hi = fmax(hi, y[e]);
-        fine = fine && isfinite(y[e]);
+        lo = y[e] < lo ? y[e] : lo;
+        hi = y[e] > hi ? y[e] : hi;
+        fine = fine && fabs(y[e]) <= 1e300;
     }
 #pragma unroll
     for (int o = HL / 2; o > 0; o >>= 1) {
-        lo = fmin(lo, __shfl_xor_sync(~0u, lo, o));
-        hi = fmax(hi, __shfl_xor_sync(~0u, hi, o));
+        const double l = __shfl_xor_sync(~0u, lo, o), h = __shfl_xor_sync(~0u, hi, o);
+        lo = l < lo ? l : lo;
+        hi = h > hi ? h : hi;
     }
     const unsigned half_lanes = ((1u << HL) - 1) << ((threadIdx.x & 31) & ~(HL - 1));
     const unsigned finite = __ballot_sync(~0u, fine);
@@ -151,19 +152,22 @@ __device__ __forceinline__ void quantize_row(const double (&y)[8], uint32_t &cod
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const double d = y[e] - z;
-        double c = fmin(fmax(floor(d * inv), -1.0), 16.0);
+        // (the clamp of the quotient only keeps the conversion in range)
+        int code = __double2int_rd(d * inv);
+        code = min(max(code, -1), 16);
         // the sign of d - (c + 1/2) s is exact in one fma; a tie goes to the even code
-        const double over = fma(-(c + 0.5), s, d);
-        int code = (int)c;
+        const double over = fma(-(code + 0.5), s, d);
         code += over > 0.0 || (over == 0.0 && (code & 1));
         codes |= (uint32_t)min(max(code, 0), 15) << (4 * e);
     }
 }
 
 // Codes (low word) and parameters of one kind of row (1: key, 2: value), in
-// fp64 from the start.  Called by whole warps; src null: no row.
+// fp64 from the start.  Called by whole warps; src null: no row.  ang: room for
+// the token's angles.
 template <int D>
-__device__ __noinline__ uint2 append_row64(const AppendArgs &a, const uint16_t *src, int kind, long long t)
+__device__ __noinline__ uint2 append_row64(const AppendArgs &a, const uint16_t *src, int kind, long long t,
+                                           Angle<double> *ang)
 {
     const int e0 = (threadIdx.x & (D / 8 - 1)) * 8;
     float x[8];
@@ -182,14 +186,20 @@ __device__ __noinline__ uint2 append_row64(const AppendArgs &a, const uint16_t *
         }
         const int n = a.rot / 2;
         if (n > 0) {
+            const double pos = a.pos[t];
+            __syncwarp();
+#pragma unroll 1
+            for (int i = threadIdx.x & 31; i < n; i += 32) {
+                Angle<double> x;
+                sincos(reduce_2pi(pos * (double)a.inv_freq[i]), &x.sin, &x.cos);
+                ang[i] = x;
+            }
+            __syncwarp();
             Angle<double> cs[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 cs[e] = {1.0, 0.0};
-                if (e0 < a.rot) {
-                    const int i = a.interleaved ? e0 / 2 + (e & 3) : e0 < n ? e0 + e : e0 - n + e;
-                    sincos(reduce_2pi((double)a.pos[t] * (double)a.inv_freq[i]), &cs[e].sin, &cs[e].cos);
-                }
+                if (e0 < a.rot) cs[e] = ang[a.interleaved ? e0 / 2 + (e & 3) : e0 < n ? e0 + e : e0 - n + e];
             }
             rope_row<D>(y, cs, e0, a.rot, a.interleaved);
         }
@@ -199,16 +209,18 @@ __device__ __noinline__ uint2 append_row64(const AppendArgs &a, const uint16_t *
     return r;
 }
 
-// The same from fp32 rows whose elements are off by at most 2^-18 of the row's
-// largest (EXACT: not at all).  Returns false in the lanes that see a border too
+// The same from fp32 rows whose elements are off by at most 36 * 2^-24 of the row's
+// largest (exact: not at all); row: the same 8 elements in memory.  Returns false in the lanes that see a border too
 // near.
 //
-// The bound, u = 2^-24: the norm's sum of squares is off by 13 u, its inverse
-// root by half of that and 4 u, each product by u: 13 u in all; sine and cosine
-// of a rounded angle by 2^-22 absolutely; with |a|, |b| up to sqrt(2) times the
-// largest element, a cos - b sin by 2 sqrt(2) (15 u + 2^-22) + u < 2^-18.
-template <int D, bool EXACT>
-__device__ __forceinline__ bool quantize_row32(const float (&y)[8], uint32_t &codes, uint32_t &par)
+// The bound, u = 2^-24: the norm's sum of squares is off by 12 u, its inverse
+// root by half of that and 4 u, each of two products by u: 12 u; sine and cosine
+// by 2 u, and 2 u more from the angle's rounding; their products by u.  |a| + |b|
+// is at most twice the row's largest element (the pair's length is kept), so
+// a cos - b sin is off by 2 (12 + 4 + 1) u + u = 35 u of it: 36 u is taken.
+template <int D>
+__device__ __forceinline__ bool quantize_row32(const float (&y)[8], const float *row, bool exact, uint32_t &codes,
+                                               uint32_t &par)
 {
     constexpr int HL = D / 16;               // lanes of a half
     constexpr float MAGIC = 12582912.f;      // 1.5 * 2^23: x + MAGIC holds the nearest whole number in its low bits
@@ -227,7 +239,7 @@ __device__ __forceinline__ bool quantize_row32(const float (&y)[8], uint32_t &co
     const unsigned half_lanes = ((1u << HL) - 1) << ((threadIdx.x & 31) & ~(HL - 1));
     const unsigned finite = __ballot_sync(~0u, nan == 0.f);
     const float top = fmaxf(fabsf(lo), fabsf(hi));
-    const float err = EXACT ? 0.f : fmaxf(top, __shfl_xor_sync(~0u, top, HL)) * 3.8146973e-6f;   // 2^-18, of the row
+    const float err = exact ? 0.f : fmaxf(top, __shfl_xor_sync(~0u, top, HL)) * (36.f / 16777216.f);   // of the row
     auto bf = [](float x) { return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x)); };
     const float range = (hi - lo) * (1.f / 15.f), slack = fmaf(range, 4.8e-7f, 0.25f * err);   // 8 u, and 2 err / 15
     const uint32_t zb = bf(lo - err), sb = bf(range - slack);
@@ -239,31 +251,30 @@ __device__ __forceinline__ bool quantize_row32(const float (&y)[8], uint32_t &co
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));   // within 1 ulp
     // quotients y / s - z / s: each product and the quotient's reciprocal are within 4 u
     const float zi = z * inv, near = 0.5f - fmaf(err, 1.01f * inv, fmaf((fabsf(z) + top) * inv, 4.8e-7f, 4e-6f));
-    float far = 0.f;
     codes = 0u;
+    unsigned close = 0u;   // elements next to a border
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float t = fmaf(y[e], inv, -zi), m = t + MAGIC;
-        far = fmaxf(far, fabsf(t - (m - MAGIC)));
+        if (!(fabsf(t - (m - MAGIC)) < near)) close |= 1u << e;
         codes += __float_as_uint(fminf(fmaxf(m, MAGIC), MAGIC + 15.f)) * (1u << (4 * e));
     }
     codes -= 0x4b400000u * 0x11111111u;   // MAGIC's own bits
     par = sb | (zb << 16);
-    if (EXACT) {
-        // elements on a border are common (bf16 numbers): the sign of the distance
-        // from a border is exact in one fma if y - z is
-        if (__any_sync(~0u, !(far < near))) {
-            codes = 0u;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float d = y[e] - z, f = floorf(d * inv), over = fmaf(-(f + 0.5f), s, d);
-                sure = sure && d + z == y[e] && y[e] - d == z;
-                const int c = (int)f + (over > 0.f || (over == 0.f && ((int)f & 1)));
-                codes |= (uint32_t)min(max(c, 0), 15) << (4 * e);
-            }
+    if (!exact) return sure && !close;
+    // on a border itself are one in 500 bf16 numbers: the sign of the distance
+    // from it is exact in one fma if x - z is
+    while (__any_sync(~0u, close)) {
+        if (close) {
+            const int e = __ffs(close) - 1;
+            const float x = row[e], d = x - z, f = floorf(d * inv);
+            // (d inv is within 1e-5 of a half: f is the code below the border)
+            const float over = fmaf(-(f + 0.5f), s, d);
+            const int c = (int)f + (over > 0.f || (over == 0.f && ((int)f & 1)));
+            sure = sure && d + z == x && x - d == z;
+            codes = (codes & ~(15u << (4 * e))) | (uint32_t)min(max(c, 0), 15) << (4 * e);
+            close &= close - 1;
         }
-    } else {
-        sure = sure && far < near;
     }
     return sure;
 }
@@ -288,6 +299,7 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_appe
     pdl_trigger();
     constexpr int LPR = D / 8, RPW = 32 / LPR, WARPS = kAppendThreads / 32;
     __shared__ Angle<float> s_ang[WARPS][D / 2];
+    __shared__ Angle<double> s_ang64[BITS == 4 ? WARPS : 1][D / 2];
     __shared__ float4 s_row[BITS == 4 ? WARPS : 1][32 * 2];   // keys on their way to 4 bits: RPW rows
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long unit = (long long)blockIdx.x * WARPS + warp;
@@ -348,37 +360,15 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_appe
     };
     // this warp's tasks of a kind whose tasks begin at `from` of all of them
     auto start = [&](int from) { return wpt == 1 ? 0 : (first + wpt - from % wpt) % wpt; };
-    // tasks of this warp to be done again in fp64 (4 bits): of keys, of values.
-    // They wait for the end: a call between the rows would have the rows' state
-    // moved to memory around it
-    uint32_t redo[2] = {0u, 0u};
-    // heads of a kind, kBatch rows at a time: row(head, channels ca and cb) says
-    // whether it was sure
-    auto rows = [&](const uint16_t *src, int heads, int tasks, int begin, uint32_t *unsure, auto &&row) {
-        uint32_t bit = 1u;
-        const uint16_t *pa = src + sub * D + ca, *pb = src + sub * D + cb;
-        for (int i = begin; i < tasks; i += kBatch * wpt) {
-            uint2 ra[kBatch], rb[kBatch];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int head = (i + u * wpt) * RPW;
-                ra[u] = rb[u] = make_uint2(0, 0);
-                if (head + sub < heads) {
-                    ra[u] = *reinterpret_cast<const uint2 *>(pa + (size_t)head * D);
-                    rb[u] = *reinterpret_cast<const uint2 *>(pb + (size_t)head * D);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int head = (i + u * wpt) * RPW;
-                if (head >= heads) break;
-                float x[8];
-                unpack8(make_uint4(ra[u].x, ra[u].y, rb[u].x, rb[u].y), x);
-                const bool act = head + sub < heads, sure = row(head + sub, act, x);
-                if (unsure && !__all_sync(~0u, sure || !act)) *unsure |= bit;
-                bit <<= 1;
-            }
+    // heads of a kind, kBatch rows at a time: row(head, channels ca and cb)
+    auto load = [&](const uint16_t *src, int head, int heads) {
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (head < heads) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(src + (size_t)head * D + ca);
+            const uint2 v = *reinterpret_cast<const uint2 *>(src + (size_t)head * D + cb);
+            r = make_uint4(u.x, u.y, v.x, v.y);
         }
+        return r;
     };
     auto put = [&](uint16_t *dst, const float (&x)[8]) {
         *reinterpret_cast<uint2 *>(dst + ca) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
@@ -399,80 +389,79 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_appe
     const int q0 = start(0);
     if (q0 < qt) {
         if (a.q_weight) weight(a.q_weight);
+        const uint16_t *src = a.q + t * a.q_stride;
         uint16_t *out = a.q_out + t * a.q_out_stride;
-        rows(a.q + t * a.q_stride, a.Hq, qt, q0, nullptr, [&](int head, bool act, float (&x)[8]) {
-            turn(x, a.q_weight, wf);
-            if (act) put(out + (size_t)head * D, x);
-            return true;
-        });
+        for (int i = q0; i < qt; i += kBatch * wpt) {
+            uint4 raw[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) raw[u] = load(src, (i + u * wpt) * RPW + sub, a.Hq);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int head = (i + u * wpt) * RPW + sub;
+                if (head - sub >= a.Hq) break;
+                float x[8];
+                unpack8(raw[u], x);
+                turn(x, a.q_weight, wf);
+                if (head < a.Hq) put(out + (size_t)head * D, x);
+            }
+        }
     }
     if (!store) return;
-    const bool plain = !a.k_weight && n == 0;   // keys as they came
-    // ---- keys
+    // ---- keys, then values: tasks qt .. qt + 2 kt - 1.  The rows of a batch go
+    // through one copy of the code (unrolled, the 4-bit form waited for its
+    // instructions)
     const uint16_t *kp = a.k + t * a.k_stride, *vp = a.v + t * a.v_stride;
-    const int k0 = start(qt);
-    if (k0 < kt) {
-        if (a.k_weight) weight(a.k_weight);
-        rows(kp, a.Hkv, kt, k0, BITS == 4 ? &redo[0] : nullptr, [&](int head, bool act, float (&x)[8]) {
-            turn(x, a.k_weight, wf);
-            const size_t at = row0 + ((size_t)head << a.Plog2);
-            if (BITS == 16) {
-                if (act) put(a.kp + at * D, x);
-                return true;
-            } else {
-                // back to 8 channels a lane, in order
-                float *r = reinterpret_cast<float *>(s_row[warp]) + sub * D;
-                __syncwarp();
-                *reinterpret_cast<float4 *>(r + ca) = make_float4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<float4 *>(r + cb) = make_float4(x[4], x[5], x[6], x[7]);
-                __syncwarp();
-                const float4 u = *reinterpret_cast<const float4 *>(r + e0), v = *reinterpret_cast<const float4 *>(r + e0 + 4);
-                const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-                uint32_t codes, par;
-                const bool sure = plain ? quantize_row32<D, true>(y, codes, par) : quantize_row32<D, false>(y, codes, par);
-                if (act) put4<D>(a.kv4 + at * Kv4<D>::REC, 1, codes, par);
-                return sure;
-            }
-        });
-    }
-    // ---- values, 8 channels a lane in order
-    const int v0 = start(qt + kt);
-    uint32_t bit = 1u;
-    for (int i = v0; i < kt; i += kBatch * wpt) {
+    const bool plain = !a.k_weight && n == 0;   // keys as they came
+    const int begin = start(qt);
+    if (begin < kt && a.k_weight) weight(a.k_weight);
+    unsigned long long redo = 0, bit = 1;   // tasks to be done again in fp64
+    for (int i = begin; i < 2 * kt; i += kBatch * wpt) {
         uint4 raw[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int head = (i + u * wpt) * RPW + sub;
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (head < a.Hkv) raw[u] = *reinterpret_cast<const uint4 *>(vp + (size_t)head * D + e0);
+            const int j = i + u * wpt, head = (j < kt ? j : j - kt) * RPW + sub;
+            raw[u] = load(j < kt ? kp : vp, j < 2 * kt ? head : a.Hkv, a.Hkv);
         }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int head = (i + u * wpt) * RPW + sub;
-            if (head - sub >= a.Hkv) break;
+#pragma unroll 1
+        for (int u = 0, j = i; u < kBatch && j < 2 * kt; ++u, j += wpt, bit <<= 1) {
+            const bool key = j < kt;
+            const int head = (key ? j : j - kt) * RPW + sub;
+            const bool act = head < a.Hkv;
             const size_t at = row0 + ((size_t)head << a.Plog2);
+            float x[8];
+            unpack8(raw[0], x);
+#pragma unroll
+            for (int v = 0; v + 1 < kBatch; ++v) raw[v] = raw[v + 1];
+            if (key) turn(x, a.k_weight, wf);
             if (BITS == 16) {
-                if (head < a.Hkv) *reinterpret_cast<uint4 *>(a.vp + at * D + e0) = raw[u];
-            } else {
-                float x[8];
-                unpack8(raw[u], x);
-                uint32_t codes, par;
-                const bool act = head < a.Hkv, sure = quantize_row32<D, true>(x, codes, par);
-                if (act) put4<D>(a.kv4 + at * Kv4<D>::REC, 2, codes, par);
-                if (!__all_sync(~0u, sure || !act)) redo[1] |= bit;
-                bit <<= 1;
+                if (act) put((key ? a.kp : a.vp) + at * D, x);
+                continue;
             }
+            // back to 8 channels a lane, in order
+            float *r = reinterpret_cast<float *>(s_row[warp]) + sub * D;
+            __syncwarp();
+            *reinterpret_cast<float4 *>(r + ca) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(r + cb) = make_float4(x[4], x[5], x[6], x[7]);
+            __syncwarp();
+            const float4 u4 = *reinterpret_cast<const float4 *>(r + e0), v4 = *reinterpret_cast<const float4 *>(r + e0 + 4);
+            const float y[8] = {u4.x, u4.y, u4.z, u4.w, v4.x, v4.y, v4.z, v4.w};
+            uint32_t codes, par;
+            const bool sure = quantize_row32<D>(y, r + e0, !key || plain, codes, par);
+            if (act) put4<D>(a.kv4 + at * Kv4<D>::REC, key ? 1 : 2, codes, par);
+            if (!__all_sync(~0u, sure || !act)) redo |= bit;
         }
     }
     if (BITS == 4) {
-        for (int kind = 1; kind <= 2; ++kind) {
+        // (at the end: a call between the rows would have their state moved to
+        // memory around it)
 #pragma unroll 1
-            for (uint32_t m = kind == 1 ? redo[0] : redo[1]; m; m &= m - 1) {
-                const int head = ((kind == 1 ? k0 : v0) + (__ffs(m) - 1) * wpt) * RPW + sub;
-                const bool act = head < a.Hkv;
-                const uint2 r = append_row64<D>(a, act ? (kind == 1 ? kp : vp) + (size_t)head * D : nullptr, kind, t);
-                if (act) put4<D>(a.kv4 + (row0 + ((size_t)head << a.Plog2)) * Kv4<D>::REC, kind, r.x, r.y);
-            }
+        for (; redo; redo &= redo - 1) {
+            const int j = begin + (__ffsll(redo) - 1) * wpt, kind = j < kt ? 1 : 2;
+            const int head = (j < kt ? j : j - kt) * RPW + sub;
+            const bool act = head < a.Hkv;
+            const uint2 r = append_row64<D>(a, act ? (j < kt ? kp : vp) + (size_t)head * D : nullptr, kind, t,
+                                            s_ang64[warp]);
+            if (act) put4<D>(a.kv4 + (row0 + ((size_t)head << a.Plog2)) * Kv4<D>::REC, kind, r.x, r.y);
         }
     }
 }
@@ -487,7 +476,7 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t s)
     // a warp per token, or more while that leaves the device short of warps
     // (32 an SM, twice): one token's heads are then taken at once
     long long wpt = (2 * 148 * 32 + a.T - 1) / a.T;
-    // (a warp keeps marks of up to 32 tasks of a kind)
+    // (a warp keeps marks of up to 64 tasks of keys and values)
     const int least = (a.Hkv + 32 * rpw - 1) / (32 * rpw);
     wpt = wpt < least ? least : wpt > tasks ? tasks : wpt;
     const long long warps = wpt * a.T;
