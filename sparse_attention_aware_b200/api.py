@@ -44,6 +44,15 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _raw_stream(index: int) -> int:
+    """Handle of torch's current stream on device ``index``."""
+    return _current_raw(index) if _current_raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+# torch's own accessor of the bare handle (current_stream builds an object: 8 us a call)
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _on_call_stream(fn):
     """When an entry point is given ``stream=``, the tensors it makes itself
     (contiguous copies of inputs, threshold tensors, default outputs, a
@@ -89,18 +98,19 @@ def kv_struct(cache, device=None) -> L.KVCacheS:
 def kv4_struct(cache: PagedCache4, device=None) -> L.KV4CacheS:
     """``kv_struct`` for a 4-bit cache."""
     kv, pt, sl = cache.kv, cache.page_table, cache.seq_lens
-    if kv.dtype != torch.uint8 or kv.dim() != 4 or not kv.is_contiguous() or kv.shape[3] <= 16:
+    n, h, p, r = kv.shape if kv.dim() == 4 else (0, 0, 0, 0)
+    if kv.dtype is not torch.uint8 or r <= 16 or not kv.is_contiguous():
         raise ValueError("4-bit KV cache: kv must be a contiguous uint8 [num_pages][Hkv][P][d + 16] tensor")
-    if pt.dtype != torch.int32 or pt.dim() != 2 or not pt.is_contiguous():
+    B, mp = pt.shape if pt.dim() == 2 else (0, 0)
+    if pt.dtype is not torch.int32 or pt.dim() != 2 or not pt.is_contiguous():
         raise ValueError("4-bit KV cache: page_table must be a contiguous int32 [B][max_pages] tensor")
-    if sl.dtype != torch.int32 or sl.dim() != 1 or sl.shape[0] != pt.shape[0] or not sl.is_contiguous():
+    if sl.dtype is not torch.int32 or sl.shape != (B,) or not sl.is_contiguous():
         raise ValueError("4-bit KV cache: seq_lens must be a contiguous int32 [B] tensor, B = %d" % pt.shape[0])
     dev = kv.device
-    if pt.device != dev or sl.device != dev or (device is not None and dev != torch.device(device)):
+    if pt.device != dev or sl.device != dev or (device is not None and dev != device):
         raise ValueError("4-bit KV cache: kv, page_table, seq_lens and the queries must be on one device, got %s"
                          % sorted({str(t.device) for t in (kv, pt, sl)} | {str(device)}))
-    n, h, p, r = kv.shape
-    return L.KV4CacheS(kv.data_ptr(), pt.data_ptr(), sl.data_ptr(), pt.shape[0], h, r - 16, p, pt.shape[1], n)
+    return L.KV4CacheS(kv.data_ptr(), pt.data_ptr(), sl.data_ptr(), B, h, r - 16, p, mp, n)
 
 
 def _geometry(cache, device=None) -> L.KVCacheS:
@@ -127,6 +137,18 @@ class Workspace:
         self.device = device
         self.buf: Optional[torch.Tensor] = None
         self._streams = []
+        self._raw = {}   # stream handles in _streams -> (aligned address of buf, bytes from there on)
+
+    def at(self, nbytes: int, raw: int, stream=None):
+        """``aligned`` for a call on the stream of handle ``raw``, without asking
+        torch for its stream object when the buffer has served it before."""
+        got = self._raw.get(raw)
+        if got is not None and got[1] >= nbytes:
+            return got
+        ptr, n = self.aligned(nbytes + 256, stream)
+        if self.buf.numel() and raw not in self._raw:
+            self._raw[raw] = (ptr.value, n)
+        return ptr.value, n
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
         if self.buf is None or self.buf.numel() < nbytes:
@@ -137,6 +159,7 @@ class Workspace:
                 for s in self._streams:
                     old.record_stream(s)
             self._streams = []
+            self._raw = {}
         if self.buf.device.type == "cuda":
             s = stream if stream is not None else torch.cuda.current_stream(self.buf.device)
             if all(s != x for x in self._streams):
@@ -165,6 +188,19 @@ class Workspace:
 
 
 _default_ws = {}
+_default_ws_at = {}   # (device index, stream handle) -> the same workspaces
+
+
+def _scratch(ws: Optional[Workspace], dev: torch.device, stream, nbytes: int):
+    """The workspace of a call (the caller's, else the default one of its device
+    and stream) and the stream's handle: (address, bytes, handle)."""
+    raw = _raw_stream(dev.index) if stream is None else stream.cuda_stream
+    if ws is None:
+        ws = _default_ws_at.get((dev.index, raw))
+        if ws is None:
+            ws = _default_ws_at[(dev.index, raw)] = _ws(None, dev, stream)
+    ptr, n = ws.at(nbytes, raw, stream)
+    return ptr, n, raw
 
 
 def _ws(ws: Optional[Workspace], device, stream=None) -> Workspace:
@@ -199,7 +235,7 @@ def workspace_bytes(op: int, cache, num_q_heads=0, k=0, num_splits=0, num_tokens
 def _need(t: torch.Tensor, shape, dtype, device, what: str) -> None:
     """A caller-provided output (or index) tensor must have exactly the layout
     the library writes: shape, dtype, contiguity and device."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.device != device:
         raise ValueError("%s: need a contiguous %s tensor of shape %s on %s, got %s %s on %s"
                          % (what, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
 
@@ -229,18 +265,13 @@ def _on_call_device(fn):
         if s is not None:
             with torch.cuda.stream(s):
                 return fn(*args, **kw)
-        dev = _device_of(args[0] if args else kw[first])
+        x = args[0] if args else kw[first]
+        dev = x.device if isinstance(x, torch.Tensor) else x.kv.device if isinstance(x, PagedCache4) else x.k.device
         if dev.type != "cuda" or dev.index == torch.cuda.current_device():
             return fn(*args, **kw)
         with torch.cuda.device(dev):
             return fn(*args, **kw)
     return call
-
-
-def _device_of(x) -> torch.device:
-    if isinstance(x, torch.Tensor):
-        return x.device
-    return x.kv.device if isinstance(x, PagedCache4) else x.k.device
 
 
 # --------------------------------------------------------------------------
@@ -370,10 +401,11 @@ def _decode_kv4(cache: PagedCache4, q, sel, scale, num_splits, out, lse, want_ls
     s = sel.struct()
     lib = L.load()
     need = lib.sa_kv4_decode_workspace_bytes(ctypes.byref(kv), Hq, num_splits)
-    wp, wn = _ws(ws, dev, stream).aligned(need, stream)
+    wp, wn, raw = _scratch(ws, dev, stream, need)
     _check(lib.sa_sparse_decode_attn_kv4(ctypes.byref(kv), q.data_ptr(), _qdtype(q), Hq, ctypes.byref(s),
                                          1.0 / math.sqrt(d) if scale is None else scale, num_splits, out.data_ptr(),
-                                         _ptr(lse), wp, wn, _stream(stream)), "sa_sparse_decode_attn_kv4")
+                                         None if lse is None else lse.data_ptr(), wp, wn, raw),
+           "sa_sparse_decode_attn_kv4")
     return out, lse
 
 
@@ -436,8 +468,8 @@ def plan_append(page_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torc
                     plan.cu_tokens.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr(),
                     plan.seq_ids.data_ptr(), B, pool.page_size, mp, pool.num_pages, pool.free_pages.numel(),
                     max_tokens)
-    wp, wn = _ws(ws, dev, stream).aligned(256, stream)
-    _check(L.load().sa_plan_append(ctypes.byref(a), wp, wn, _stream(stream)), "sa_plan_append")
+    wp, wn, raw = _scratch(ws, dev, stream, 256)
+    _check(L.load().sa_plan_append(ctypes.byref(a), wp, wn, raw), "sa_plan_append")
     return plan
 
 
@@ -446,9 +478,9 @@ def _rows(x: torch.Tensor, what: str, shape, device):
     tokens a multiple of 8 elements apart, 16-byte aligned (parts of a packed
     projection are taken as they are; other layouts are copied) -- and the
     elements between its tokens."""
-    if x.dtype != torch.bfloat16:
+    if x.dtype is not torch.bfloat16:
         raise TypeError("rope_append: %s must be bf16, got %s" % (what, x.dtype))
-    if tuple(x.shape) != shape or x.device != device:
+    if x.shape != shape or x.device != device:
         raise ValueError("rope_append: %s must be %s on %s, got %s on %s"
                          % (what, shape, device, tuple(x.shape), x.device))
     st, sh, sd = x.stride()
@@ -508,10 +540,10 @@ def rope_append(cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positi
                       None if rot == 0 else inv_freq.data_ptr(), None if q_weight is None else q_weight.data_ptr(),
                       None if k_weight is None else k_weight.data_ptr(), L.DTYPE_F32 if wt == torch.float32 else
                       L.DTYPE_BF16, eps, T, Hq, rot, int(interleaved))
-    wp, wn = _ws(ws, dev, stream).aligned(256, stream)
+    wp, wn, raw = _scratch(ws, dev, stream, 256)
     lib = L.load()
     fn = lib.sa_rope_append_kv4 if four else lib.sa_rope_append
-    _check(fn(ctypes.byref(kv), ctypes.byref(a), wp, wn, _stream(stream)),
+    _check(fn(ctypes.byref(kv), ctypes.byref(a), wp, wn, raw),
            "sa_rope_append_kv4" if four else "sa_rope_append")
     return q_out
 
@@ -534,9 +566,9 @@ def expand_kv4(cache: PagedCache4, pages: torch.Tensor, k: Optional[torch.Tensor
         v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     else:
         _need(v, shape, torch.bfloat16, dev, "expand_kv4 v")
-    wp, wn = _ws(ws, dev, stream).aligned(256, stream)
+    wp, wn, raw = _scratch(ws, dev, stream, 256)
     _check(L.load().sa_expand_kv4(ctypes.byref(kv), pages.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(), wp, wn,
-                                  _stream(stream)), "sa_expand_kv4")
+                                  raw), "sa_expand_kv4")
     return k, v
 
 

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
     const int B = a.B, P = 1 << a.Plog2, tid = threadIdx.x;
     int *s_old = plan_sm;            // [B] tokens held
     int *s_new = s_old + B;          // [B] tokens to come, -1 = ended
-    int *s_need = s_new + B;         // [B] fresh pages of earlier sequences
+    int *s_need = s_new + B;         // [B] fresh pages of earlier sequences (of an ended one: freed pages)
     int *s_cu = s_need + B;          // [B + 1]
     const int rank = (int)cg::this_cluster().block_rank(), ranks = (int)cg::this_cluster().num_blocks();
     const long long Lcap = (long long)a.max_pages << a.Plog2;
@@ -132,22 +132,26 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
         if (b >= B) continue;
         const Sums x = plus(before, part[u]);
         s_cu[b] = bad ? 0 : (int)x.tok;
-        s_need[b] = (int)x.need;
-        // pages of an ended sequence onto the stack (few sequences end in a step)
-        if (!bad && s_new[b] < 0) {
+        s_need[b] = (int)(s_new[b] < 0 ? x.back : x.need);
+    }
+    if (tid == 0) s_cu[B] = (int)all.tok;
+    __syncthreads();
+    const int gtid = rank * kPlanThreads + tid, threads = ranks * kPlanThreads, lane = tid & 31;
+    if (!bad && all.back > 0) {
+        // pages of ended sequences onto the stack, a warp a sequence
+        for (int b = gtid >> 5; b < B; b += threads >> 5) {
+            if (s_new[b] >= 0) continue;
             const int held = (s_old[b] + P - 1) >> a.Plog2;
-            for (int p = rank; p < held; p += ranks) {
+            for (int p = lane; p < held; p += 32) {
                 const int page = a.table[(size_t)b * a.max_pages + p];
                 if (page < 0 || page >= a.num_pages) fault(a.st, CHK_PAGE, page);
-                a.free[count + x.back + p] = page;
+                a.free[count + s_need[b] + p] = page;
             }
         }
     }
-    if (tid == 0) s_cu[B] = (int)all.tok;
     cg::this_cluster().sync();   // every CTA has read the inputs; the stack is whole
 
     // ---- lengths, prefix sums, fresh table entries
-    const int gtid = rank * kPlanThreads + tid, threads = ranks * kPlanThreads;
     for (int b = gtid; b < B; b += threads) {
         const int add = s_new[b];
         a.sl_out[b] = bad ? s_old[b] : add < 0 ? 0 : s_old[b] + add;
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
             const int old = s_old[b], add = s_new[b];
             if (add <= 0) continue;
             const int held = (old + P - 1) >> a.Plog2, then = (old + add + P - 1) >> a.Plog2;
-            for (int p = held + (gtid & 31); p < then; p += 32) {
+            for (int p = held + lane; p < then; p += 32) {
                 int page = a.free[top - 1 - (s_need[b] + p - held)];
                 if (page < 0 || page >= a.num_pages) {
                     fault(a.st, CHK_PAGE, page);
@@ -172,28 +176,50 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
             }
         }
     }
-    // ---- tokens
-    const int total = (int)all.tok;
-    for (int i = gtid; i < a.max_tokens; i += threads) {
-        int pos = 0, seq = -1;
-        long long slot = -1;
-        if (i < total) {
-            int lo = 0, hi = B - 1;   // the last b with cu_b <= i holds i (empty ones before it have the same cu)
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (s_cu[mid] <= i) lo = mid; else hi = mid - 1;
-            }
-            seq = lo;
-            pos = s_old[seq] + i - s_cu[seq];
-            const int held = (s_old[seq] + P - 1) >> a.Plog2, p = pos >> a.Plog2;
-            const int page = p < held ? a.table[(size_t)seq * a.max_pages + p]
-                                      : a.free[top - 1 - (s_need[seq] + p - held)];
-            if (page < 0 || page >= a.num_pages) fault(a.st, CHK_PAGE, page);
-            else slot = ((long long)page << a.Plog2) + (pos & (P - 1));
+    // ---- tokens: a run of them per warp, kRows rows of 32 at a time, so that
+    // the sequence is searched for once and the page lookups overlap
+    constexpr int kRows = 4;
+    const int total = (int)all.tok, warps = threads >> 5;
+    const int run = (a.max_tokens + warps * 32 - 1) / (warps * 32) * 32;
+    const int end = (int)min((long long)a.max_tokens, (long long)run * ((gtid >> 5) + 1));
+    int seq = 0;
+    {
+        int lo = 0, hi = B - 1;   // the last b with cu_b <= i holds i (empty ones before it have the same cu)
+        const int i = run * (gtid >> 5) + lane;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_cu[mid] <= i) lo = mid; else hi = mid - 1;
         }
-        a.pos[i] = pos;
-        a.slots[i] = slot;
-        if (a.seq_ids) a.seq_ids[i] = seq;
+        seq = lo;
+    }
+    for (int i0 = run * (gtid >> 5) + lane; i0 < end; i0 += 32 * kRows) {
+        int pos[kRows], of[kRows], page[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int i = i0 + 32 * u;
+            pos[u] = 0;
+            of[u] = -1;
+            page[u] = -1;
+            if (i >= total || i >= end) continue;
+            while (s_cu[seq + 1] <= i) ++seq;
+            of[u] = seq;
+            pos[u] = s_old[seq] + i - s_cu[seq];
+            const int held = (s_old[seq] + P - 1) >> a.Plog2, p = pos[u] >> a.Plog2;
+            page[u] = p < held ? a.table[(size_t)seq * a.max_pages + p] : a.free[top - 1 - (s_need[seq] + p - held)];
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int i = i0 + 32 * u;
+            if (i >= end) break;
+            long long slot = -1;
+            if (of[u] >= 0) {
+                if (page[u] < 0 || page[u] >= a.num_pages) fault(a.st, CHK_PAGE, page[u]);
+                else slot = ((long long)page[u] << a.Plog2) + (pos[u] & (P - 1));
+            }
+            a.pos[i] = pos[u];
+            a.slots[i] = slot;
+            if (a.seq_ids) a.seq_ids[i] = of[u];
+        }
     }
 }
 
@@ -202,9 +228,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
 cudaError_t launch_plan(const PlanArgs &a, cudaStream_t s)
 {
     const size_t smem = (size_t)(4 * a.B + 1) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(k_plan_append, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (4 * kPlanMaxBatch + 1) * (int)sizeof(int));
-    if (e != cudaSuccess) return e;
+    if (smem > 40960) {   // (static shared memory comes on top, up to 48 KB together without asking)
+        cudaError_t e = cudaFuncSetAttribute(k_plan_append, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (4 * kPlanMaxBatch + 1) * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+    }
     const int ctas = a.max_tokens > 4 * kPlanThreads || a.B > kPlanThreads ? 8 : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
