@@ -44,6 +44,41 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _load_fast():
+    """The native short way of the calls below (csrc/fastcall.cpp), set up with
+    libsa's entry points; None where it has not been built."""
+    try:
+        from . import _fastcall
+    except ImportError:
+        return None
+    lib = L.load()
+    _fastcall.init(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
+                     ("sa_plan_append", "sa_rope_append", "sa_rope_append_kv4", "sa_expand_kv4",
+                      "sa_sparse_decode_attn_kv4", "sa_kv4_decode_workspace_bytes")))
+    return _fastcall
+
+
+_fast = False   # False: not looked for yet
+
+
+def _short(ws: Optional[Workspace], device, stream):
+    """(native calls, workspace address, bytes, stream handle) if a call may go
+    the short way: it is on torch's current stream, with a workspace that has
+    served that stream before."""
+    global _fast
+    if _fast is False:
+        _fast = _load_fast()
+    if _fast is None or stream is not None or device.type != "cuda":
+        return None
+    raw = _raw_stream(device.index)
+    if ws is None:
+        ws = _default_ws_at.get((device.index, raw))
+        if ws is None:
+            return None
+    at = ws._raw.get(raw)
+    return None if at is None else (_fast, at[0], at[1], raw)
+
+
 def _raw_stream(index: int) -> int:
     """Handle of torch's current stream on device ``index``."""
     return _current_raw(index) if _current_raw is not None else torch.cuda.current_stream(index).cuda_stream
@@ -380,8 +415,25 @@ def sparse_decode_attn(cache, q: torch.Tensor, sel, scale: Optional[float] = Non
     return out, lse
 
 
-@_on_call_device
 def _decode_kv4(cache: PagedCache4, q, sel, scale, num_splits, out, lse, want_lse, ws, stream):
+    if out is None and lse is None:
+        way = _short(ws, q.device, stream)
+        if way is not None:
+            tok = isinstance(sel, TokenSelection)
+            if tok or isinstance(sel, BlockSelection):
+                fast, wp, wn, raw = way
+                got = fast.decode(cache.kv, cache.page_table, cache.seq_lens, q, sel.idx if tok else sel.blocks,
+                                  sel.count if tok else sel.block_counts, L.SEL_TOKENS if tok else L.SEL_BLOCKS, scale,
+                                  num_splits, want_lse, wp, wn, raw)
+                if got is not None:
+                    if isinstance(got, int):
+                        _check(got, "sa_sparse_decode_attn_kv4")
+                    return got
+    return _decode_kv4_checked(cache, q, sel, scale, num_splits, out, lse, want_lse, ws, stream)
+
+
+@_on_call_device
+def _decode_kv4_checked(cache: PagedCache4, q, sel, scale, num_splits, out, lse, want_lse, ws, stream):
     B, Hq, d = q.shape
     dev = q.device
     kv = kv4_struct(cache, dev)
@@ -428,7 +480,6 @@ class AppendPlan:
                           torch.empty(max_tokens, dtype=torch.int32, device=device))
 
 
-@_on_call_device
 def plan_append(page_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torch.Tensor, pool: PagePool,
                 max_tokens: int, seq_lens_out: Optional[torch.Tensor] = None,
                 free_count_out: Optional[torch.Tensor] = None, plan: Optional[AppendPlan] = None,
@@ -439,6 +490,23 @@ def plan_append(page_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torc
     and so are ``seq_lens`` and ``pool.free_count`` unless ``seq_lens_out`` /
     ``free_count_out`` take the new values.  A step that does not fit changes
     nothing, gives every token slot -1 and is recorded in the workspace."""
+    if plan is None:
+        way = _short(ws, page_table.device, stream)
+        if way is not None:
+            fast, wp, wn, raw = way
+            got = fast.plan(page_table, seq_lens, new_lens, pool.free_pages, pool.free_count, pool.num_pages,
+                            pool.page_size, max_tokens, seq_lens_out, free_count_out, wp, wn, raw)
+            if got is not None:
+                if isinstance(got, int):
+                    _check(got, "sa_plan_append")
+                return AppendPlan(*got)
+    return _plan_append(page_table, seq_lens, new_lens, pool, max_tokens, seq_lens_out, free_count_out, plan, ws,
+                        stream=stream)
+
+
+@_on_call_device
+def _plan_append(page_table, seq_lens, new_lens, pool, max_tokens, seq_lens_out, free_count_out, plan, ws,
+                 stream=None) -> AppendPlan:
     dev = page_table.device
     if page_table.dim() != 2:
         raise ValueError("plan_append: page_table must be int32 [B][max_pages]")
@@ -490,7 +558,6 @@ def _rows(x: torch.Tensor, what: str, shape, device):
     return x, (st if shape[0] > 1 else shape[1] * shape[2])
 
 
-@_on_call_device
 def rope_append(cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
                 slots: torch.Tensor, inv_freq: Optional[torch.Tensor] = None,
                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
@@ -502,6 +569,25 @@ def rope_append(cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positi
     q [T][Hq][d], k and v [T][Hkv][d] bf16; positions int32 [T]; slots int64 [T]
     (-1: not stored); inv_freq fp32 [rot_dim / 2], None for no rotation.  Returns
     the queries, bf16 [T][Hq][d] (in ``q_out`` if given, which may be ``q``)."""
+    if q_out is None:
+        way = _short(ws, q.device, stream)
+        if way is not None:
+            fast, wp, wn, raw = way
+            four = isinstance(cache, PagedCache4)
+            got = fast.append(cache.kv if four else cache.k, None if four else cache.v, cache.page_table,
+                              cache.seq_lens, q, k, v, positions, slots, inv_freq, q_weight, k_weight, eps, interleaved,
+                              wp, wn, raw)
+            if got is not None:
+                if isinstance(got, int):
+                    _check(got, "sa_rope_append_kv4" if four else "sa_rope_append")
+                return got
+    return _rope_append(cache, q, k, v, positions, slots, inv_freq, q_weight, k_weight, eps, interleaved, q_out, ws,
+                        stream=stream)
+
+
+@_on_call_device
+def _rope_append(cache, q, k, v, positions, slots, inv_freq, q_weight, k_weight, eps, interleaved, q_out, ws,
+                 stream=None) -> torch.Tensor:
     four = isinstance(cache, PagedCache4)
     dev = q.device
     if q.dim() != 3:
@@ -548,12 +634,25 @@ def rope_append(cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positi
     return q_out
 
 
-@_on_call_device
 def expand_kv4(cache: PagedCache4, pages: torch.Tensor, k: Optional[torch.Tensor] = None,
                v: Optional[torch.Tensor] = None, ws: Optional[Workspace] = None, stream=None):
     """Pages of a 4-bit cache as bf16 pages (``sa_expand_kv4``): ``pages`` int32
     [n] (-1: that output page is left as it was) -> (k, v) bf16 [n][Hkv][P][d],
     pools that a PagedCache can hold."""
+    if k is None and v is None:
+        way = _short(ws, pages.device, stream)
+        if way is not None:
+            fast, wp, wn, raw = way
+            got = fast.expand(cache.kv, cache.page_table, cache.seq_lens, pages, wp, wn, raw)
+            if got is not None:
+                if isinstance(got, int):
+                    _check(got, "sa_expand_kv4")
+                return got
+    return _expand_kv4(cache, pages, k, v, ws, stream=stream)
+
+
+@_on_call_device
+def _expand_kv4(cache, pages, k, v, ws, stream=None):
     dev = cache.kv.device
     kv = kv4_struct(cache)
     shape = (pages.numel(), kv.num_kv_heads, kv.page_size, kv.head_dim)

@@ -1,4 +1,4 @@
-"""Build libsa.so in-tree with nvcc for sm_100a.
+"""Build libsa.so in-tree with nvcc for sm_100a, and the binding's _fastcall.so.
 
     python -m sparse_attention_aware_b200.build [--force] [--ptxas-verbose]
 """
@@ -8,12 +8,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsa.so")
+FAST = os.path.join(PKG, "_fastcall.so")
+FAST_SRC = os.path.join(CSRC, "fastcall.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -37,7 +40,29 @@ def nvcc() -> str:
     return "nvcc"
 
 
+def build_fastcall(force: bool = False) -> str:
+    """The short calls of the binding, a Python module against torch's own
+    libraries (already loaded by whoever imports it)."""
+    deps = [FAST_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(FAST) and all(os.path.getmtime(p) <= os.path.getmtime(FAST) for p in deps):
+        return FAST
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = FAST + ".tmp.%d" % os.getpid()
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.sep in nvcc() else "/usr/local/cuda"
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
+                    "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+                    "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
+                    "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                    "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+                    FAST_SRC, "-o", tmp, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cuda",
+                    "-ltorch_cpu", "-lc10", "-lc10_cuda"], check=True)
+    os.replace(tmp, FAST)
+    return FAST
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    build_fastcall(force)
     if not force and not _stale():
         return LIB
     tmp = LIB + ".tmp.%d" % os.getpid()
