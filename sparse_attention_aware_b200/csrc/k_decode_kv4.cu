@@ -182,6 +182,14 @@ __device__ __forceinline__ int split_at(int n, int s, int S, int least, int long
     return n - min(n, ((int)((float)n * left) + unit - 1) & ~(unit - 1));
 }
 
+// Column c of an output row from its whole state
+__device__ __forceinline__ void finish(const DecodeArgs &a, size_t row, int D, int c, float M, float Ls, float O)
+{
+    const bool some = Ls != 0.f;
+    a.out[row * D + c] = f2bf(some ? O / Ls : 0.f);
+    if (a.lse && c == 0) a.lse[row] = some ? (M + lg2(Ls)) * kLn2 : -INFINITY;
+}
+
 // NH = 8-head column blocks of the CTA (1 or 2); TOKENS: one query head and
 // its token list, else a kv head's heads and the sequence's block list
 template <int D, int NH, bool QF32, bool TOKENS>
@@ -253,12 +261,23 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 3 : 2) k_decode_kv4(const
         lo = split_at(n, s, a.S, kLeast >> a.c.Plog2, kLong >> a.c.Plog2, 1);
         hi = split_at(n, s + 1, a.S, kLeast >> a.c.Plog2, kLong >> a.c.Plog2, 1);
     }
-    if (lo >= hi) {   // nothing for this split: an empty partial, which the combine skips
-        for (int j = tid; j < nheads; j += kDThreads) {
-            const size_t row = (size_t)b * a.Hq + h0 + j;
-            a.part_ml[(row * a.S + s) * 2 + 0] = -INFINITY;
-            a.part_ml[(row * a.S + s) * 2 + 1] = 0.f;
+    // what this CTA has of an output row's column: the output itself where there
+    // is one split, else a part for the combine kernel
+    auto leave = [&](int j, int c, float M, float Ls, float O) {
+        const size_t row = (size_t)b * a.Hq + h0 + j;
+        if (a.S == 1) {
+            finish(a, row, D, c, M, Ls, O);
+            return;
         }
+        a.part_o[(row * a.S + s) * D + c] = O;
+        if (c == 0) {
+            a.part_ml[(row * a.S + s) * 2 + 0] = M;
+            a.part_ml[(row * a.S + s) * 2 + 1] = Ls;
+        }
+    };
+    if (lo >= hi) {   // nothing for this split (the combine skips an empty part's output)
+        for (int i = tid; i < (a.S == 1 ? nheads * D : nheads); i += kDThreads)
+            leave(a.S == 1 ? i / D : i, a.S == 1 ? i % D : 0, -INFINITY, 0.f, 0.f);
         return;
     }
 
@@ -701,39 +720,34 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 3 : 2) k_decode_kv4(const
             O = fmaf(wgt, mo[(w * 16 + j) * D + c], O);
             Ls = fmaf(wgt, lw, Ls);
         }
-        const size_t row = (size_t)b * a.Hq + h0 + j;
-        a.part_o[(row * a.S + s) * D + c] = O;
-        if (c == 0) {
-            a.part_ml[(row * a.S + s) * 2 + 0] = M;
-            a.part_ml[(row * a.S + s) * 2 + 1] = Ls;
-        }
+        leave(j, c, M, Ls, O);
     }
 }
 
 // Merge of the splits, as k_decode_combine, except that a split whose sum is
 // not a number (a selected row was stored as NaN) makes the result NaN.
+// (Joined by a cluster of the splits in the first kernel instead, a masked
+// step took 13.2 us and not 11.7: CTAs of a cluster start and end together.)
 template <int D>
-__global__ void __launch_bounds__(D) k_kv4_combine(const float *__restrict__ part_o, const float *__restrict__ part_ml,
-                                                    int S, uint16_t *__restrict__ out, float *__restrict__ lse)
+__global__ void __launch_bounds__(D) k_kv4_combine(const DecodeArgs a)
 {
     pdl_wait();
     pdl_trigger();
-    const int row = blockIdx.x, c = threadIdx.x;
-    const float *ml = part_ml + (size_t)row * S * 2;
+    const int c = threadIdx.x;
+    const size_t row = blockIdx.x;
+    const float *ml = a.part_ml + row * a.S * 2;
     float M = -INFINITY;
-    for (int s = 0; s < S; ++s)
+    for (int s = 0; s < a.S; ++s)
         if (ml[2 * s + 1] != 0.f) M = fmaxf(M, ml[2 * s]);
     float o = 0.f, Ls = 0.f;
-    for (int s = 0; s < S; ++s) {
+    for (int s = 0; s < a.S; ++s) {
         const float ls = ml[2 * s + 1];
         if (ls == 0.f) continue;
         const float w = ex2(ml[2 * s] - M);
         Ls = fmaf(w, ls, Ls);
-        o = fmaf(w, part_o[((size_t)row * S + s) * D + c], o);
+        o = fmaf(w, a.part_o[(row * a.S + s) * D + c], o);
     }
-    const bool some = Ls != 0.f;
-    out[(size_t)row * D + c] = f2bf(some ? o / Ls : 0.f);
-    if (lse && c == 0) lse[row] = some ? (M + lg2(Ls)) * kLn2 : -INFINITY;
+    finish(a, row, D, c, M, Ls, o);
 }
 
 template <int D, int NH, bool QF32, bool TOKENS>
@@ -744,7 +758,9 @@ cudaError_t launch_kv4(const DecodeArgs &a, cudaStream_t s)
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
     const int hpg = a.Hq / a.c.Hkv;
     const dim3 grid((unsigned)(TOKENS ? a.Hq : a.c.Hkv * ((hpg + 15) / 16)), (unsigned)a.c.B, (unsigned)a.S);
-    return launch_pdl(kern, grid, dim3(kDThreads), smem, s, a);
+    if (cudaError_t e = launch_pdl(kern, grid, dim3(kDThreads), smem, s, a)) return e;
+    if (a.S == 1) return cudaSuccess;
+    return launch_pdl(k_kv4_combine<D>, dim3((unsigned)(a.c.B * a.Hq)), dim3(D), 0, s, a);
 }
 
 template <int D, bool QF32>
@@ -773,13 +789,8 @@ int decode_kv4_splits(int B, int rows, long long list)
 cudaError_t launch_decode_kv4(const DecodeArgs &a, cudaStream_t s)
 {
     if (a.c.B * a.Hq == 0) return cudaSuccess;
-    cudaError_t e;
-    if (a.c.D == 64) e = a.q_f32 ? launch_kind<64, true>(a, s) : launch_kind<64, false>(a, s);
-    else e = a.q_f32 ? launch_kind<128, true>(a, s) : launch_kind<128, false>(a, s);
-    if (e != cudaSuccess) return e;
-    auto comb = a.c.D == 64 ? k_kv4_combine<64> : k_kv4_combine<128>;
-    return launch_pdl(comb, dim3((unsigned)(a.c.B * a.Hq)), dim3((unsigned)a.c.D), 0, s, a.part_o, a.part_ml, a.S, a.out,
-                      a.lse);
+    if (a.c.D == 64) return a.q_f32 ? launch_kind<64, true>(a, s) : launch_kind<64, false>(a, s);
+    return a.q_f32 ? launch_kind<128, true>(a, s) : launch_kind<128, false>(a, s);
 }
 
 }  // namespace sa
