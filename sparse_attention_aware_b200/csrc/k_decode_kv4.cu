@@ -52,6 +52,7 @@
 //
 // Bound: HBM for long lists; the widening and the softmax take about 60% of
 // the issue slots at that rate.
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "kv4.cuh"
@@ -70,7 +71,11 @@ template <int D>
 struct DSmem {
     static constexpr int STAGE = kDR * Kv4<D>::REC;
     static constexpr int RING = kDW * kDST * STAGE;
-    static constexpr int MERGE = kDW * (16 * D + 32) * 4;   // per-warp O, m, l (up to 16 heads)
+    // merge: per-warp O, m, l of up to 16 heads.  Two rows of ROW floats are 8
+    // banks apart, so the warps' 16-byte writes (4 heads' rows, 2 runs of 4
+    // channels) touch all banks once
+    static constexpr int ROW = D + 4;
+    static constexpr int MERGE = kDW * (16 * ROW + 32) * 4;
     static constexpr int BYTES = RING > MERGE ? RING : MERGE;
 };
 
@@ -182,18 +187,21 @@ __device__ __forceinline__ int split_at(int n, int s, int S, int least, int long
     return n - min(n, ((int)((float)n * left) + unit - 1) & ~(unit - 1));
 }
 
-// Column c of an output row from its whole state
-__device__ __forceinline__ void finish(const DecodeArgs &a, size_t row, int D, int c, float M, float Ls, float O)
+// Columns c .. c + 3 of an output row from its whole state
+__device__ __forceinline__ void finish(const DecodeArgs &a, size_t row, int D, int c, float M, float Ls, const float4 &O)
 {
     const bool some = Ls != 0.f;
-    a.out[row * D + c] = f2bf(some ? O / Ls : 0.f);
+    const float f = some ? 1.f / Ls : 0.f;
+    const __nv_bfloat162 u = __floats2bfloat162_rn(O.x * f, O.y * f), v = __floats2bfloat162_rn(O.z * f, O.w * f);
+    *reinterpret_cast<uint2 *>(a.out + row * D + c) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
     if (a.lse && c == 0) a.lse[row] = some ? (M + lg2(Ls)) * kLn2 : -INFINITY;
 }
 
 // NH = 8-head column blocks of the CTA (1 or 2); TOKENS: one query head and
 // its token list, else a kv head's heads and the sequence's block list
 template <int D, int NH, bool QF32, bool TOKENS>
-__global__ void __launch_bounds__(kDThreads, NH == 1 ? 3 : 2) k_decode_kv4(const DecodeArgs a)
+__global__ void __launch_bounds__(kDThreads, NH == 1 ? (TOKENS && !QF32 ? 4 : 3) : 2) k_decode_kv4(const DecodeArgs a)
 {
     pdl_wait();
     pdl_trigger();
@@ -261,23 +269,24 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 3 : 2) k_decode_kv4(const
         lo = split_at(n, s, a.S, kLeast >> a.c.Plog2, kLong >> a.c.Plog2, 1);
         hi = split_at(n, s + 1, a.S, kLeast >> a.c.Plog2, kLong >> a.c.Plog2, 1);
     }
-    // what this CTA has of an output row's column: the output itself where there
+    // what this CTA has of 4 columns of an output row: the output itself where there
     // is one split, else a part for the combine kernel
-    auto leave = [&](int j, int c, float M, float Ls, float O) {
+    auto leave = [&](int j, int c, float M, float Ls, const float4 &O) {
         const size_t row = (size_t)b * a.Hq + h0 + j;
         if (a.S == 1) {
             finish(a, row, D, c, M, Ls, O);
             return;
         }
-        a.part_o[(row * a.S + s) * D + c] = O;
+        *reinterpret_cast<float4 *>(a.part_o + (row * a.S + s) * D + c) = O;
         if (c == 0) {
             a.part_ml[(row * a.S + s) * 2 + 0] = M;
             a.part_ml[(row * a.S + s) * 2 + 1] = Ls;
         }
     };
     if (lo >= hi) {   // nothing for this split (the combine skips an empty part's output)
-        for (int i = tid; i < (a.S == 1 ? nheads * D : nheads); i += kDThreads)
-            leave(a.S == 1 ? i / D : i, a.S == 1 ? i % D : 0, -INFINITY, 0.f, 0.f);
+        const int per = a.S == 1 ? D / 4 : 1;
+        for (int i = tid; i < nheads * per; i += kDThreads)
+            leave(i / per, i % per * 4, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
         return;
     }
 
@@ -675,26 +684,25 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 3 : 2) k_decode_kv4(const
                 zs[1][nh][j] += __shfl_xor_sync(~0u, zs[1][nh][j], off);
             }
     __syncthreads();
-    float *mo = reinterpret_cast<float *>(sm);                 // [warp][16][D]
-    float *mm = mo + kDW * 16 * D;                              // [warp][16]
+    constexpr int ROW = SM::ROW;
+    float *mo = reinterpret_cast<float *>(sm);                 // [warp][16][ROW]
+    float *mm = mo + kDW * 16 * ROW;                            // [warp][16]
     float *ml = mm + kDW * 16;                                  // [warp][16]
-    // (a token list has one head, column 0; for the others all columns are
-    // written, since a test of each costs more)
+    // (a token list has one head, column 0)
     if (!TOKENS || tq == 0) {
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
+        for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-                for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-                    for (int i = 0; i < 4; i += TOKENS ? 2 : 1) {
-                        const int h = nh * 8 + 2 * tq + (i & 1), half = cb / CBH;
-                        const int c = cb * 32 + 4 * gq + 2 * j + (i >> 1);
-                        // (rows gq + 8 hold odd channels, whose codes went in as 16 c)
-                        mo[(warp * 16 + h) * D + c] = fmaf(o[cb][j][nh][i] * ((i >> 1) ? 1048576.f : 16777216.f),
-                                                           1.f / keep[half], zs[half][nh][i & 1]);
-                    }
+                for (int i = 0; i < (TOKENS ? 1 : 2); ++i) {
+                    // channels 4gq .. 4gq + 3 of block cb; the odd ones (rows gq + 8) went in as 16 c
+                    const int half = cb / CBH;
+                    const float f = 16777216.f / keep[half], odd = f * 0.0625f, z = zs[half][nh][i];
+                    *reinterpret_cast<float4 *>(mo + (warp * 16 + nh * 8 + 2 * tq + i) * ROW + cb * 32 + 4 * gq) =
+                        make_float4(fmaf(o[cb][0][nh][i], f, z), fmaf(o[cb][0][nh][2 + i], odd, z),
+                                    fmaf(o[cb][1][nh][i], f, z), fmaf(o[cb][1][nh][2 + i], odd, z));
+                }
     }
     if (gq == 0) {
 #pragma unroll
@@ -706,18 +714,23 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 3 : 2) k_decode_kv4(const
             }
     }
     __syncthreads();
-    for (int i = tid; i < nheads * D; i += kDThreads) {
-        const int j = i / D, c = i % D;
+    for (int i = tid; i < nheads * (D / 4); i += kDThreads) {
+        const int j = i / (D / 4), c = i % (D / 4) * 4;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kDW; ++w) M = fmaxf(M, mm[w * 16 + j]);
-        float O = 0.f, Ls = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        float Ls = 0.f;
 #pragma unroll
         for (int w = 0; w < kDW; ++w) {
             const float lw = ml[w * 16 + j];
             if (lw == 0.f) continue;   // no token (a sum that is not a number is taken along)
             const float wgt = ex2(mm[w * 16 + j] - M);
-            O = fmaf(wgt, mo[(w * 16 + j) * D + c], O);
+            const float4 x = *reinterpret_cast<const float4 *>(mo + (w * 16 + j) * ROW + c);
+            O.x = fmaf(wgt, x.x, O.x);
+            O.y = fmaf(wgt, x.y, O.y);
+            O.z = fmaf(wgt, x.z, O.z);
+            O.w = fmaf(wgt, x.w, O.w);
             Ls = fmaf(wgt, lw, Ls);
         }
         leave(j, c, M, Ls, O);
@@ -729,25 +742,37 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? 3 : 2) k_decode_kv4(const
 // (Joined by a cluster of the splits in the first kernel instead, a masked
 // step took 13.2 us and not 11.7: CTAs of a cluster start and end together.)
 template <int D>
-__global__ void __launch_bounds__(D) k_kv4_combine(const DecodeArgs a)
+__global__ void __launch_bounds__(128) k_kv4_combine(const DecodeArgs a, int rows)
 {
     pdl_wait();
     pdl_trigger();
-    const int c = threadIdx.x;
-    const size_t row = blockIdx.x;
-    const float *ml = a.part_ml + row * a.S * 2;
+    constexpr int LANES = D / 4;   // of a row
+    const int r = blockIdx.x * (128 / LANES) + threadIdx.x / LANES, c = threadIdx.x % LANES * 4;
+    if (r >= rows) return;
+    const size_t row = r;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + row * a.S;
+    const float *po = a.part_o + row * a.S * D + c;
     float M = -INFINITY;
-    for (int s = 0; s < a.S; ++s)
-        if (ml[2 * s + 1] != 0.f) M = fmaxf(M, ml[2 * s]);
-    float o = 0.f, Ls = 0.f;
+#pragma unroll 4
     for (int s = 0; s < a.S; ++s) {
-        const float ls = ml[2 * s + 1];
-        if (ls == 0.f) continue;
-        const float w = ex2(ml[2 * s] - M);
-        Ls = fmaf(w, ls, Ls);
-        o = fmaf(w, a.part_o[(row * a.S + s) * D + c], o);
+        const float2 x = ml[s];
+        if (x.y != 0.f) M = fmaxf(M, x.x);
     }
-    finish(a, row, D, c, M, Ls, o);
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    float Ls = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < a.S; ++s) {
+        const float2 x = ml[s];
+        if (x.y == 0.f) continue;
+        const float w = ex2(x.x - M);
+        const float4 v = *reinterpret_cast<const float4 *>(po + (size_t)s * D);
+        Ls = fmaf(w, x.y, Ls);
+        O.x = fmaf(w, v.x, O.x);
+        O.y = fmaf(w, v.y, O.y);
+        O.z = fmaf(w, v.z, O.z);
+        O.w = fmaf(w, v.w, O.w);
+    }
+    finish(a, row, D, c, M, Ls, O);
 }
 
 template <int D, int NH, bool QF32, bool TOKENS>
@@ -760,7 +785,8 @@ cudaError_t launch_kv4(const DecodeArgs &a, cudaStream_t s)
     const dim3 grid((unsigned)(TOKENS ? a.Hq : a.c.Hkv * ((hpg + 15) / 16)), (unsigned)a.c.B, (unsigned)a.S);
     if (cudaError_t e = launch_pdl(kern, grid, dim3(kDThreads), smem, s, a)) return e;
     if (a.S == 1) return cudaSuccess;
-    return launch_pdl(k_kv4_combine<D>, dim3((unsigned)(a.c.B * a.Hq)), dim3(D), 0, s, a);
+    const int rows = a.c.B * a.Hq, per = 128 / (D / 4);
+    return launch_pdl(k_kv4_combine<D>, dim3((unsigned)((rows + per - 1) / per)), dim3(128), 0, s, a, rows);
 }
 
 template <int D, bool QF32>
