@@ -36,7 +36,11 @@
 namespace sa {
 namespace {
 
-constexpr int kAppendThreads = 256;
+// One warp a block: a warp that has rows to do again takes several times as
+// long, and must not hold the places of others (blocks of 8 warps: 118 us for a
+// 32768-token prompt into bf16 pages, 147 us for 16391 tokens into 4-bit pages
+// and back; of one: 110 and 127 us).
+constexpr int kAppendThreads = 32;
 
 template <typename F>
 struct Angle {
@@ -82,7 +86,7 @@ __device__ __forceinline__ void rope_row(F (&x)[8], const Angle<F> (&cs)[8], int
             }
         }
     } else {
-        const int n = rot / 2, lane = threadIdx.x & 31;
+        const int n = rot / 2, lane = threadIdx.x;
         const int src = e0 < n ? lane + n / 8 : e0 < rot ? lane - n / 8 : lane;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -137,7 +141,7 @@ __device__ __forceinline__ void quantize_row(const double (&y)[8], uint32_t &cod
         lo = l < lo ? l : lo;
         hi = h > hi ? h : hi;
     }
-    const unsigned half_lanes = ((1u << HL) - 1) << ((threadIdx.x & 31) & ~(HL - 1));
+    const unsigned half_lanes = ((1u << HL) - 1) << ((threadIdx.x) & ~(HL - 1));
     const unsigned finite = __ballot_sync(~0u, fine);
     const __nv_bfloat16 zb = __float2bfloat16_rn((float)lo), sb = __float2bfloat16_rn((float)((hi - lo) / 15.0));
     const float zf = __bfloat162float(zb), sf = __bfloat162float(sb);
@@ -189,7 +193,7 @@ __device__ __noinline__ uint2 append_row64(const AppendArgs &a, const uint16_t *
             const double pos = a.pos[t];
             __syncwarp();
 #pragma unroll 1
-            for (int i = threadIdx.x & 31; i < n; i += 32) {
+            for (int i = threadIdx.x; i < n; i += 32) {
                 Angle<double> x;
                 sincos(reduce_2pi(pos * (double)a.inv_freq[i]), &x.sin, &x.cos);
                 ang[i] = x;
@@ -236,7 +240,7 @@ __device__ __forceinline__ bool quantize_row32(const float (&y)[8], const float 
         lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
     }
-    const unsigned half_lanes = ((1u << HL) - 1) << ((threadIdx.x & 31) & ~(HL - 1));
+    const unsigned half_lanes = ((1u << HL) - 1) << ((threadIdx.x) & ~(HL - 1));
     const unsigned finite = __ballot_sync(~0u, nan == 0.f);
     const float top = fmaxf(fabsf(lo), fabsf(hi));
     const float err = exact ? 0.f : fmaxf(top, __shfl_xor_sync(~0u, top, HL)) * (36.f / 16777216.f);   // of the row
@@ -293,19 +297,17 @@ constexpr int kBatch = 4;   // rows a lane has in flight
 
 // wpt warps share a token's heads
 template <int D, int BITS>
-__global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_append(const AppendArgs a, int wpt)
+__global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 24 : 32) k_rope_append(const AppendArgs a, int wpt)
 {
     pdl_wait();
     pdl_trigger();
-    constexpr int LPR = D / 8, RPW = 32 / LPR, WARPS = kAppendThreads / 32;
-    __shared__ Angle<float> s_ang[WARPS][D / 2];
-    __shared__ Angle<double> s_ang64[BITS == 4 ? WARPS : 1][D / 2];
-    __shared__ float4 s_row[BITS == 4 ? WARPS : 1][32 * 2];   // keys on their way to 4 bits: RPW rows
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long unit = (long long)blockIdx.x * WARPS + warp;
-    const long long t = unit / wpt;
-    const int first = (int)(unit - t * wpt);
-    if (t >= a.T) return;
+    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    __shared__ Angle<float> s_ang[D / 2];
+    __shared__ Angle<double> s_ang64[BITS == 4 ? D / 2 : 1];
+    __shared__ float4 s_row[BITS == 4 ? 32 * 2 : 1];   // rows on their way to 4 bits: RPW of them
+    const int lane = threadIdx.x;
+    const long long t = blockIdx.x / wpt;
+    const int first = (int)(blockIdx.x - t * wpt);
     const int gl = lane & (LPR - 1), sub = lane / LPR, e0 = gl * 8;
     const int qt = (a.Hq + RPW - 1) / RPW, kt = (a.Hkv + RPW - 1) / RPW;
     const int n = a.rot / 2;
@@ -328,12 +330,12 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_appe
         for (int i = lane; i < n; i += 32) {
             Angle<float> x;
             sincosf((float)reduce_2pi(pos * (double)a.inv_freq[i]), &x.sin, &x.cos);
-            s_ang[warp][i] = x;
+            s_ang[i] = x;
         }
         __syncwarp();
         if (turns) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) cs[e] = s_ang[warp][4 * gl + e];
+            for (int e = 0; e < 4; ++e) cs[e] = s_ang[4 * gl + e];
         }
     }
 
@@ -438,7 +440,7 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_appe
                 continue;
             }
             // back to 8 channels a lane, in order
-            float *r = reinterpret_cast<float *>(s_row[warp]) + sub * D;
+            float *r = reinterpret_cast<float *>(s_row) + sub * D;
             __syncwarp();
             *reinterpret_cast<float4 *>(r + ca) = make_float4(x[0], x[1], x[2], x[3]);
             *reinterpret_cast<float4 *>(r + cb) = make_float4(x[4], x[5], x[6], x[7]);
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 3 : 4) k_rope_appe
             const int head = (j < kt ? j : j - kt) * RPW + sub;
             const bool act = head < a.Hkv;
             const uint2 r = append_row64<D>(a, act ? (j < kt ? kp : vp) + (size_t)head * D : nullptr, kind, t,
-                                            s_ang64[warp]);
+                                            s_ang64);
             if (act) put4<D>(a.kv4 + (row0 + ((size_t)head << a.Plog2)) * Kv4<D>::REC, kind, r.x, r.y);
         }
     }
@@ -479,8 +481,7 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t s)
     // (a warp keeps marks of up to 64 tasks of keys and values)
     const int least = (a.Hkv + 32 * rpw - 1) / (32 * rpw);
     wpt = wpt < least ? least : wpt > tasks ? tasks : wpt;
-    const long long warps = wpt * a.T;
-    const dim3 grid((unsigned)((warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32)));
+    const dim3 grid((unsigned)(wpt * a.T));   // at most max(a.T, 9472 + a.T, least a.T) blocks
     auto kern = a.kv4 ? (a.D == 64 ? k_rope_append<64, 4> : k_rope_append<128, 4>)
                       : (a.D == 64 ? k_rope_append<64, 16> : k_rope_append<128, 16>);
     return launch_pdl(kern, grid, dim3(kAppendThreads), 0, s, a, (int)wpt);
