@@ -26,6 +26,7 @@ namespace sa {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kRows = 4;   // rows of 32 pages or tokens that a warp has in flight
 constexpr int kPlanItems = kPlanMaxBatch / kPlanThreads;   // sequences per thread
 
 struct Sums {
@@ -142,10 +143,17 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
         for (int b = gtid >> 5; b < B; b += threads >> 5) {
             if (s_new[b] >= 0) continue;
             const int held = (s_old[b] + P - 1) >> a.Plog2;
-            for (int p = lane; p < held; p += 32) {
-                const int page = a.table[(size_t)b * a.max_pages + p];
-                if (page < 0 || page >= a.num_pages) fault(a.st, CHK_PAGE, page);
-                a.free[count + s_need[b] + p] = page;
+            for (int p = lane; p < held; p += 32 * kRows) {
+                int page[kRows];
+#pragma unroll
+                for (int u = 0; u < kRows; ++u)
+                    page[u] = p + 32 * u < held ? a.table[(size_t)b * a.max_pages + p + 32 * u] : 0;
+#pragma unroll
+                for (int u = 0; u < kRows; ++u) {
+                    if (p + 32 * u >= held) break;
+                    if (page[u] < 0 || page[u] >= a.num_pages) fault(a.st, CHK_PAGE, page[u]);
+                    a.free[count + s_need[b] + p + 32 * u] = page[u];
+                }
             }
         }
     }
@@ -166,19 +174,25 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
             const int old = s_old[b], add = s_new[b];
             if (add <= 0) continue;
             const int held = (old + P - 1) >> a.Plog2, then = (old + add + P - 1) >> a.Plog2;
-            for (int p = held + lane; p < then; p += 32) {
-                int page = a.free[top - 1 - (s_need[b] + p - held)];
-                if (page < 0 || page >= a.num_pages) {
-                    fault(a.st, CHK_PAGE, page);
-                    page = -1;
+            const int *from = a.free + top - 1 - s_need[b] + held;
+            for (int p = held + lane; p < then; p += 32 * kRows) {
+                int page[kRows];
+#pragma unroll
+                for (int u = 0; u < kRows; ++u) page[u] = p + 32 * u < then ? from[-(p + 32 * u)] : 0;
+#pragma unroll
+                for (int u = 0; u < kRows; ++u) {
+                    if (p + 32 * u >= then) break;
+                    if (page[u] < 0 || page[u] >= a.num_pages) {
+                        fault(a.st, CHK_PAGE, page[u]);
+                        page[u] = -1;
+                    }
+                    a.table[(size_t)b * a.max_pages + p + 32 * u] = page[u];
                 }
-                a.table[(size_t)b * a.max_pages + p] = page;
             }
         }
     }
-    // ---- tokens: a run of them per warp, kRows rows of 32 at a time, so that
-    // the sequence is searched for once and the page lookups overlap
-    constexpr int kRows = 4;
+    // ---- tokens: a run of them per warp, so that the sequence is searched for
+    // once, kRows rows at a time, so that the page lookups overlap
     const int total = (int)all.tok, warps = threads >> 5;
     const int run = (a.max_tokens + warps * 32 - 1) / (warps * 32) * 32;
     const int end = (int)min((long long)a.max_tokens, (long long)run * ((gtid >> 5) + 1));
@@ -233,7 +247,13 @@ cudaError_t launch_plan(const PlanArgs &a, cudaStream_t s)
                                              (4 * kPlanMaxBatch + 1) * (int)sizeof(int));
         if (e != cudaSuccess) return e;
     }
-    const int ctas = a.max_tokens > 4 * kPlanThreads || a.B > kPlanThreads ? 8 : 1;
+    // a step's few tokens need one CTA (4.7 us for 32); 131072 take 11.7 us with
+    // 16 CTAs and 14.8 with 8
+    const int ctas = a.max_tokens > 32 * kPlanThreads ? 16 : a.max_tokens > 4 * kPlanThreads || a.B > kPlanThreads ? 8 : 1;
+    if (ctas > 8) {
+        cudaError_t e = cudaFuncSetAttribute(k_plan_append, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kPlanThreads);
