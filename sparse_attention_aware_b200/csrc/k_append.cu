@@ -58,17 +58,19 @@ __device__ __forceinline__ double reduce_2pi(double x)
 __device__ __forceinline__ float inv_root(float x) { return rsqrtf(x); }   // within 2 ulps
 __device__ __forceinline__ double inv_root(double x) { return 1.0 / sqrt(x); }
 
+// Returns mean x^2 + eps
 template <int D, typename F>
-__device__ __forceinline__ void norm_row(F (&x)[8], const F (&w)[8], float eps)
+__device__ __forceinline__ F norm_row(F (&x)[8], const F (&w)[8], float eps)
 {
     F ss = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fma(x[e], x[e], ss);
 #pragma unroll
     for (int o = D / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-    const F r = inv_root(ss * (F)(1.0 / D) + (F)eps);
+    const F mean = ss * (F)(1.0 / D) + (F)eps, r = inv_root(mean);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
+    return mean;
 }
 
 // cs: the lane's 8 angles (pairs apart: angle of channel e; pairs together:
@@ -339,9 +341,14 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 24 : 32) k_rope_ap
         }
     }
 
-    // norm and rotation of a row: x[0..3] at channel ca, x[4..7] at cb
+    // norm and rotation of a row: x[0..3] at channel ca, x[4..7] at cb; false
+    // where squares leave the range that fp32 holds well
     auto turn = [&](float (&x)[8], const void *w, const float (&wf)[8]) {
-        if (w) norm_row<D>(x, wf, a.eps);
+        bool held = true;
+        if (w) {
+            const float mean = norm_row<D>(x, wf, a.eps);
+            held = mean > 1e-24f && mean < 1e30f;
+        }
         if (a.interleaved) {
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
@@ -359,6 +366,7 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 24 : 32) k_rope_ap
                 x[4 + p] = fmaf(v, cs[p].cos, u * cs[p].sin);
             }
         }
+        return held;
     };
     // this warp's tasks of a kind whose tasks begin at `from` of all of them
     auto start = [&](int from) { return wpt == 1 ? 0 : (first + wpt - from % wpt) % wpt; };
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 24 : 32) k_rope_ap
             unpack8(raw[0], x);
 #pragma unroll
             for (int v = 0; v + 1 < kBatch; ++v) raw[v] = raw[v + 1];
-            if (key) turn(x, a.k_weight, wf);
+            const bool held = key ? turn(x, a.k_weight, wf) : true;
             if (BITS == 16) {
                 if (act) put((key ? a.kp : a.vp) + at * D, x);
                 continue;
@@ -448,7 +456,7 @@ __global__ void __launch_bounds__(kAppendThreads, BITS == 4 ? 24 : 32) k_rope_ap
             const float4 u4 = *reinterpret_cast<const float4 *>(r + e0), v4 = *reinterpret_cast<const float4 *>(r + e0 + 4);
             const float y[8] = {u4.x, u4.y, u4.z, u4.w, v4.x, v4.y, v4.z, v4.w};
             uint32_t codes, par;
-            const bool sure = quantize_row32<D>(y, r + e0, !key || plain, codes, par);
+            const bool sure = quantize_row32<D>(y, r + e0, !key || plain, codes, par) && held;
             if (act) put4<D>(a.kv4 + at * Kv4<D>::REC, key ? 1 : 2, codes, par);
             if (!__all_sync(~0u, sure || !act)) redo |= bit;
         }

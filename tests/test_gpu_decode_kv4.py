@@ -71,7 +71,10 @@ BLOCK_CASES = [  # seed, B, Hq, Hkv, d, page, lens, spans per sequence, splits, 
     (15, 1, 20, 1, 128, 64, [1111], [[(1, 2), (63, 65), (128, 1100)]], 3, False),
     (16, 2, 40, 1, 64, 64, [700, 65], [[(0, 700)], [(64, 65)]], 2, False),
     (17, 2, 64, 8, 128, 16, [4100, 1500], [[(0, 4), (3076, 4100)], [(988, 1500)]], 0, False),
-    (18, 1, 4, 4, 128, 64, [6000], [[(0, 6000)]], 64, False)]
+    (18, 1, 4, 4, 128, 64, [6000], [[(0, 6000)]], 64, False),
+    (19, 2, 4, 2, 128, 16, [4100, 3], [[(0, 4100)], [(0, 3)]], 1, False),
+    (20, 1, 3, 1, 64, 16, [5555], [[(1, 5554)]], 3, True),
+    (26, 1, 16, 1, 128, 64, [9000], [[(0, 9000)]], 2, True)]
 
 
 @pytest.mark.parametrize("seed,B,H,hkv,d,page,lens,spans,splits,f32", BLOCK_CASES)
@@ -113,6 +116,58 @@ def test_scores_far_apart(cuda_dev):
         for splits in (1, 5):
             got = sa.sparse_decode_attn(_gpu(kv, table, sl, cuda_dev), q.to(cuda_dev), sel, 1.0, splits)
             R.check_decode(got, R.decode(kv, table, q, lambda b, h: t, 1.0))
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+def test_value_scales_far_apart(cuda_dev, splits):
+    """Value rows from 2^-40 to 2^20 of one another, rising, falling and mixed, with
+    the weight on small ones: each head's error stays within its own rows' share."""
+    d, page, n = 128, 16, 700
+    for order in ("rising", "falling", "mixed"):
+        g, kv, table, sl = _cache(27, 1, 1, d, page, [n])
+        e = torch.linspace(-40, 20, n).double()
+        e = e if order == "rising" else e.flip(0) if order == "falling" else e[torch.randperm(n, generator=g)]
+        v = torch.randn(n, d, generator=g).double() * 2.0 ** e[:, None]
+        k = torch.randn(n, d, generator=g).double() * 0.05
+        k[:, 0] -= 0.08 * (e + 40) / 60 * 40     # the larger the values, the smaller the weight
+        t = torch.arange(n)
+        kv[table[0, t // page].long(), 0, t % page] = R.records(k, v)
+        q = torch.zeros(1, 2, d)
+        q[:, :, 0], q[:, 1, 1] = 10.0, 1.0
+        blocks, cnt = R.pack_entries([R.entries_of([(0, n)], n, page)])
+        sel = sa.BlockSelection(blocks.to(cuda_dev), cnt.to(cuda_dev))
+        out, lse = sa.sparse_decode_attn(_gpu(kv, table, sl, cuda_dev), q.to(cuda_dev), sel, 1.0, splits)
+        ref = R.decode(kv, table, q, lambda b, h: t, 1.0)
+        # share of row t in the output: its weight times its largest value; each is kept
+        # to 2^-11 (2^-8 in all with the bf16 output), or to 2^-31 of the largest scale
+        rk, rv, s = R.values(kv[table[0, t // page].long(), 0, t % page])
+        for h in range(2):
+            w = torch.softmax(rk @ q[0, h].double(), 0)
+            share = (w[:, None] * (rv.abs() + 15 * s[:, 1].repeat_interleave(d // 2, 1))).sum(0)
+            lim = 2.0 ** -10 * share + R.BF16_HALF * ref[0][0, h].abs() + w.sum() * 2.0 ** -31 * float(s[:, 1].max()) * 15
+            err = (out[0, h].double().cpu() - ref[0][0, h]).abs()
+            assert bool((err <= lim).all()), (order, h, float((err / lim).max()))
+
+
+def test_calls_on_two_streams(cuda_dev):
+    """Decodes queued on two streams at once, without workspaces, equal the same calls alone."""
+    g, kv, table, sl = _cache(28, 3, 2, 128, 16, [3000, 700, 1999])
+    c = _gpu(kv, table, sl, cuda_dev)
+    blocks, cnt = R.pack_entries([R.entries_of([(0, n)], n, 16) for n in (3000, 700, 1999)])
+    sel = sa.BlockSelection(blocks.to(cuda_dev), cnt.to(cuda_dev))
+    qs = torch.randn(2, 20, 3, 8, 128, generator=g).bfloat16().to(cuda_dev)
+    alone = [[sa.sparse_decode_attn(c, q, sel, num_splits=5) for q in side] for side in qs]
+    torch.cuda.synchronize(cuda_dev)
+    streams = [torch.cuda.Stream(cuda_dev) for _ in range(2)]
+    got = [[], []]
+    for i in range(20):
+        for j, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[j].append(sa.sparse_decode_attn(c, qs[j, i], sel, num_splits=5))
+    torch.cuda.synchronize(cuda_dev)
+    for a, b in zip(alone, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
 
 
 def test_unordered_and_repeated_tokens(cuda_dev):

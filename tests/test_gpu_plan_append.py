@@ -66,6 +66,39 @@ def test_plan_matches_plain(cuda_dev, seed, B, page, most, in_place):
         assert torch.equal(dl.cpu(), old) and int(pool.free_count) == count
 
 
+def test_plan_of_long_prompts(cuda_dev):
+    """More tokens than one CTA, or eight, take: the same as the plain form."""
+    for seed, B, page, most, cap in ((21, 300, 64, 2000, 40001), (22, 9, 16, 9000, 131072), (23, 70, 16, 900, 8000)):
+        g = torch.Generator().manual_seed(seed)
+        table, old, _, free, _, _ = _problem(seed, B, page, most)
+        new = torch.randint(0, 2 * (cap // B), (B,), generator=g)
+        new[::7] = -1
+        new[new.clamp(min=0).cumsum(0) > cap] = 0
+        new = new.int()
+        held = (old + page - 1) // page
+        per = int(((old + new.clamp(min=0) + page - 1) // page).max()) + 1
+        total = int(held.sum()) + cap // page + B + 5
+        perm = torch.randperm(total, generator=g).int()
+        table, at = torch.full((B, per), -77, dtype=torch.int32), 0
+        for b, h in enumerate(held.tolist()):
+            table[b, :h] = perm[at:at + h]
+            at += h
+        free = torch.full((total,), -55, dtype=torch.int32)
+        free[:total - at] = perm[at:]
+        (t, lens, f, n), ref = R.plan(table, old, new, free, total - at, page, cap)
+        ws = sa.Workspace(cuda_dev)
+        dt, dl, df = table.to(cuda_dev), old.to(cuda_dev), free.to(cuda_dev)
+        pool = sa.PagePool(df, torch.tensor([total - at], dtype=torch.int32, device=cuda_dev), total, page)
+        for _ in range(2):                       # and again through the binding's short way, undone in between
+            p = sa.plan_append(dt, dl, new.to(cuda_dev), pool, cap, ws=ws)
+            assert ws.status()[0] == 0
+            assert torch.equal(dt.cpu(), t) and torch.equal(dl.cpu(), lens) and int(pool.free_count) == n
+            assert torch.equal(df.cpu()[:n], f[:n])
+            for x, y in zip((p.cu_tokens, p.positions, p.slots, p.seq_ids), ref):
+                assert torch.equal(x.cpu(), y)
+            dt.copy_(table), dl.copy_(old), df.copy_(free), pool.free_count.fill_(total - at)
+
+
 def test_plan_empty(cuda_dev):
     i32 = dict(dtype=torch.int32, device=cuda_dev)
     pool = sa.PagePool.full(4, 16, cuda_dev)
@@ -155,7 +188,8 @@ def _check_rows(got, ref, where):
 CASES = [  # T, Hq, Hkv, d, page, rot, interleaved, norm
     (1, 4, 4, 64, 16, 64, False, True), (1, 64, 8, 128, 16, 128, False, True), (5, 32, 8, 128, 64, 128, True, True),
     (3, 5, 1, 128, 16, 64, False, True), (17, 12, 3, 64, 16, 32, True, False), (33, 8, 2, 128, 64, 0, False, True),
-    (700, 7, 3, 128, 16, 128, False, False), (301, 3, 2, 64, 64, 48, False, True), (2, 1, 1, 128, 16, 16, True, True)]
+    (700, 7, 3, 128, 16, 128, False, False), (301, 3, 2, 64, 64, 48, False, True), (2, 1, 1, 128, 16, 16, True, True),
+    (9999, 5, 3, 64, 64, 64, False, True), (9601, 4, 9, 128, 16, 32, True, True), (2, 2, 300, 128, 64, 128, False, True)]
 
 
 @pytest.mark.parametrize("T,hq,hkv,d,page,rot,il,norm", CASES)
@@ -247,6 +281,27 @@ def test_4bit_rows_that_are_special(cuda_dev, d):
         f = ~torch.isnan(b)
         # bf16 of zero + scale code by way of fp32: half a step, and 2^-24
         assert bool(((a - b)[f].abs() <= (R.BF16_HALF + 2.0 ** -23) * b[f].abs() + 1e-45).all())
+
+
+@pytest.mark.parametrize("d,eps", [(64, 0.0), (128, 0.0), (128, 1e-6), (128, 1e30)])
+def test_4bit_keys_of_every_size(cuda_dev, d, eps):
+    """Keys whose squares overflow or vanish in fp32 still store the bytes of the 64-bit definition."""
+    g = torch.Generator().manual_seed(int(d + 1e3 * min(eps, 1)))
+    size = 10.0 ** torch.arange(-36, 37, 4).double()
+    T = len(size)
+    x = (torch.randn(T, 2, d, generator=g).double() * size[:, None, None]).bfloat16()
+    x[3, 1, 5:] = 0                                                  # a row with few elements
+    w = (1 + 0.2 * torch.randn(d, generator=g)).bfloat16()
+    pos = torch.arange(T).int() * 1000
+    inv = (10000.0 ** (-torch.arange(0, d, 2).double() / d)).float()
+    c = sa.PagedCache4.empty(2, 2, 64, d, torch.zeros(1, 1, dtype=torch.int32, device=cuda_dev),
+                             torch.zeros(1, dtype=torch.int32, device=cuda_dev))
+    xd = x.to(cuda_dev)
+    sa.rope_append(c, xd, xd, xd, pos.to(cuda_dev), torch.arange(T, device=cuda_dev), inv.to(cuda_dev),
+                   k_weight=w.to(cuda_dev), eps=eps)
+    # (eps reaches the library as fp32)
+    ref = R.records(R.norm_rope(x, w, float(torch.tensor(eps, dtype=torch.float32)), pos, inv, False), x.double())
+    assert torch.equal(c.kv.cpu()[0, :, :T].transpose(0, 1), ref)
 
 
 def test_append_in_place_strided_and_on_a_stream(cuda_dev):
