@@ -1,14 +1,17 @@
 /*
- * sa.h -- C ABI of libsa: head-aware sparse attention over a paged bf16 KV
- * cache, built for NVIDIA B200 (sm_100a).
+ * sa.h -- C ABI of libsa: head-aware sparse attention over a paged KV cache
+ * (bf16, or 4 bits), built for NVIDIA B200 (sm_100a).
  *
- * The library implements the two parts of the method:
+ * The library implements the two parts of the method, and the step around
+ * them:
  *   - selection: exact per-head top-k on an anchor layer (Kascade), the
  *     two-branch centroid / radius-rescue block score (RBS-Attention), and
  *     block-aligned span masks (Declarative Attention focus/local/global,
  *     LoZA streaming window);
- *   - sparse attention: split-KV decode with a combine pass, and causal
- *     block-sparse prefill on tcgen05 tensor cores.
+ *   - sparse attention: split-KV decode with a combine pass, over bf16 or
+ *     4-bit pages, and causal block-sparse prefill on tcgen05 tensor cores;
+ *   - a serving step's tokens: pages and slots from the sequences' lengths,
+ *     per-head norm, rotary positions and the store into the cache.
  *
  * Sources (page titles; sections named per entry point below):
  *  [Kascade] "Kascade稀疏注意力：让长上下文大模型更快落地物流供应链"

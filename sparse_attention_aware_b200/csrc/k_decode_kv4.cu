@@ -19,9 +19,10 @@
 // 4-7 is 16 c 2^-24, and fp16 products are exact, so eight codes cost one
 // shift and four masks.  The 16 goes into the query (a sixteenth of those
 // channels) or out of the sums (those rows of O), the 2^24 into the factors.
-// Measured at 32 sequences x 8 kv heads, 409 MB of records: 146 us with bf16
+// Before, at 32 sequences x 8 kv heads, 435 MB of records: 146 us with bf16
 // numbers 1 + c/16 (one logic operation and one shift a pair, all on the
-// integer pipe), 118 us with fp16 numbers c - 8 (a mask-or and an fma a pair).
+// integer pipe), 118 us with fp16 numbers c - 8 (a mask-or and an fma a pair),
+// 95 us with the codes as they are, all else equal.
 //
 // Ranges.  A query is scaled by a power of two per head so that its largest
 // element lies in [2^9, 2^10): fp16 then holds a bf16 query exactly down to
@@ -50,8 +51,15 @@
 // score passes it by more than 8 in the base-2 domain: weights stay below 2^8,
 // and most tiles need neither the max across lanes nor a rescale.
 //
-// Bound: HBM for long lists; the widening and the softmax take about 60% of
-// the issue slots at that rate.
+// Measured (B200, 6.55 TB/s copy): every page of 32 sequences of up to 16384
+// tokens, 32 heads on 8 kv heads (435 MB) 92 us, 0.72 of HBM; 1024 lists of 4096
+// of 65536 tokens 144 us (0.58 by the rows' own bytes; a row's 144 bytes touch
+// 192 in 64-byte pieces, and by those it is 0.84); a masked step of 4 sequences
+// 12 us, 256 of 4096 tokens of 4 heads 4.7 us.  The copies alone take 70 and 131
+// us, the arithmetic alone 88 and 127: about 290 instructions per 16 rows, of
+// which no part dominates (leaving out the widening, or half of a product, saves
+// 8 us of 92 each), with 12 to 16 warps an SM.  Short calls are bound by the
+// dependent trips length -> entry -> page -> rows -> merge.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -195,7 +203,7 @@ __device__ __forceinline__ void finish(const DecodeArgs &a, size_t row, int D, i
     const __nv_bfloat162 u = __floats2bfloat162_rn(O.x * f, O.y * f), v = __floats2bfloat162_rn(O.z * f, O.w * f);
     *reinterpret_cast<uint2 *>(a.out + row * D + c) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
-    if (a.lse && c == 0) a.lse[row] = some ? (M + lg2(Ls)) * kLn2 : -INFINITY;
+    if (a.lse && c == 0) a.lse[row] = some ? (M + log2f(Ls)) * kLn2 : -INFINITY;
 }
 
 // NH = 8-head column blocks of the CTA (1 or 2); TOKENS: one query head and
@@ -740,7 +748,7 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? (TOKENS && !QF32 ? 4 : 3)
 // Merge of the splits, as k_decode_combine, except that a split whose sum is
 // not a number (a selected row was stored as NaN) makes the result NaN.
 // (Joined by a cluster of the splits in the first kernel instead, a masked
-// step took 13.2 us and not 11.7: CTAs of a cluster start and end together.)
+// step took 13.2 us and not 11.8: CTAs of a cluster start and end together.)
 template <int D>
 __global__ void __launch_bounds__(128) k_kv4_combine(const DecodeArgs a, int rows)
 {

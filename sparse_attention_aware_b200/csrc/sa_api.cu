@@ -168,7 +168,7 @@ size_t ws_prefill(const sa_kv_cache *kv, int Hq, int T)
 
 extern "C" {
 
-int32_t sa_version(void) { return 100; }
+int32_t sa_version(void) { return 200; }
 
 const char *sa_status_string(sa_status s)
 {
