@@ -246,8 +246,9 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? (TOKENS && !QF32 ? 4 : 3)
             if (h < nheads) query8<QF32>(a.q, ((size_t)b * a.Hq + h0 + h) * D + cb * 32 + tq * 8, qx[nh][cb]);
         }
     }
+    // (both lengths in one trip, before either is looked at)
     const int Lcap = a.c.max_pages << a.c.Plog2;
-    int L = __ldg(a.c.sl + b);
+    int L = __ldg(a.c.sl + b), n = TOKENS ? __ldg(a.cnt + (size_t)b * a.Hq + h0) : __ldg(a.ecnt + b);
     if (L < 0 || L > Lcap) {
         if (reports) fault(st, CHK_SEQ_LEN, L);
         L = L < 0 ? 0 : Lcap;
@@ -259,7 +260,6 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? (TOKENS && !QF32 ? 4 : 3)
     const int *idx = nullptr;
     if (TOKENS) {
         const size_t r = (size_t)b * a.Hq + h0;
-        int n = __ldg(a.cnt + r);
         if (n < 0 || n > a.kcap) {
             if (reports) fault(st, CHK_COUNT, n);
             n = n < 0 ? 0 : a.kcap;
@@ -268,7 +268,6 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? (TOKENS && !QF32 ? 4 : 3)
         lo = split_at(n, s, a.S, kLeast, kLong, kDR);
         hi = split_at(n, s + 1, a.S, kLeast, kLong, kDR);
     } else {
-        int n = __ldg(a.ecnt + b);
         if (n < 0 || n > a.max_blocks) {
             if (reports) fault(st, CHK_BLOCK_ENTRY, n);
             n = n < 0 ? 0 : a.max_blocks;
