@@ -110,6 +110,8 @@ def kv_struct(cache, device=None) -> L.KVCacheS:
     (k/v bf16 [num_pages][Hkv][P][d], page_table int32 [B][max_pages],
     seq_lens int32 [B]).  ``device``: when given, every cache tensor must be on
     it (the device of the call's queries).  Raises ValueError otherwise."""
+    if isinstance(cache, PagedCache4):
+        raise TypeError("this call reads bf16 pages: expand_kv4 gives those of a 4-bit cache")
     k, v = cache.k, cache.v
     pt, sl = cache.page_table, cache.seq_lens
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
@@ -386,14 +388,18 @@ def select_topk(cache, q: torch.Tensor, k: int, idx: Optional[torch.Tensor] = No
 
 
 @_on_call_stream
-def sparse_decode_attn(cache, q: torch.Tensor, sel, scale: Optional[float] = None, num_splits: int = 1,
+def sparse_decode_attn(cache, q: torch.Tensor, sel, scale: Optional[float] = None,
+                       num_splits: Optional[int] = None,
                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                        want_lse: bool = True, ws: Optional[Workspace] = None, stream=None):
     """Split-KV sparse decode + combine (``sa_sparse_decode_attn``, or
-    ``sa_sparse_decode_attn_kv4`` over a PagedCache4, where ``num_splits=0``
-    lets the library choose).  Returns (out bf16, lse fp32)."""
+    ``sa_sparse_decode_attn_kv4`` over a PagedCache4).  ``num_splits`` parts a
+    list, 1 by default; over a PagedCache4 0, the default there, lets the
+    library choose.  Returns (out bf16, lse fp32)."""
     if isinstance(cache, PagedCache4):
-        return _decode_kv4(cache, q, sel, scale, num_splits, out, lse, want_lse, ws, stream)
+        return _decode_kv4(cache, q, sel, scale, 0 if num_splits is None else num_splits, out, lse, want_lse, ws, stream)
+    if num_splits is None:
+        num_splits = 1
     B, Hq, d = q.shape
     dev = q.device
     scale = 1.0 / math.sqrt(d) if scale is None else scale

@@ -118,6 +118,67 @@ def test_scores_far_apart(cuda_dev):
             R.check_decode(got, R.decode(kv, table, q, lambda b, h: t, 1.0))
 
 
+@pytest.mark.parametrize("scale,size", [(0.0, 1.0), (-0.15, 1.0), (0.09, 1e-25), (0.09, 0.0), (1e-12, 1e12)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_scales_and_queries_of_every_size(cuda_dev, scale, size, f32):
+    """A scale of zero or below, queries far below and above one, and of zeros."""
+    g, kv, table, sl = _cache(29, 2, 2, 64, 16, [90, 333])
+    q = torch.randn(2, 6, 64, generator=g) * size
+    q[1, 3] = 0
+    q = q if f32 else q.bfloat16()
+    blocks, cnt = R.pack_entries([R.entries_of([(0, n)], n, 16) for n in (90, 333)])
+    idx = torch.arange(90).int().expand(2, 6, 90).contiguous()
+    for sel, toks in ((sa.BlockSelection(blocks.to(cuda_dev), cnt.to(cuda_dev)), lambda b, h: torch.arange((90, 333)[b])),
+                      (sa.TokenSelection(idx.to(cuda_dev), torch.full((2, 6), 90, dtype=torch.int32, device=cuda_dev)),
+                       lambda b, h: torch.arange(90))):
+        got = sa.sparse_decode_attn(_gpu(kv, table, sl, cuda_dev), q.to(cuda_dev), sel, scale)
+        R.check_decode(got, R.decode(kv, table, q, toks, scale))
+
+
+def test_a_pool_past_32_bits(cuda_dev):
+    """Records, bf16 rows and slots whose byte offsets pass 2^32: append, expand and decode there."""
+    d, page, hkv, T = 128, 64, 1, 150
+    g = torch.Generator().manual_seed(30)
+    pages = 520_000                              # 4.8 GB of records
+    high = torch.tensor([519_999, 480_001, 470_003], dtype=torch.int32)
+    slots = (high.long()[torch.arange(T) // page] * page + torch.arange(T) % page).to(cuda_dev)
+    assert int(slots.min()) * (d + 16) > 2 ** 32
+    x = torch.randn(T, 3, d, generator=g).bfloat16()
+    table, lens = high[None].to(cuda_dev), torch.tensor([T], dtype=torch.int32, device=cuda_dev)
+    pos = torch.arange(T).int()
+    inv = (10000.0 ** (-torch.arange(0, d, 2).double() / d)).float()
+    kv = torch.zeros(pages, hkv, page, d + 16, dtype=torch.uint8, device=cuda_dev)
+    c = sa.PagedCache4(kv, table, lens)
+    xd = x.to(cuda_dev)
+    ws = sa.Workspace(cuda_dev)
+    q = sa.rope_append(c, xd[:, :1], xd[:, 1:2], xd[:, 2:], pos.to(cuda_dev), slots, inv.to(cuda_dev), ws=ws)
+    rec = R.records(R.norm_rope(x[:, 1:2], None, 0, pos, inv, False), x[:, 2:].double())
+    assert torch.equal(kv[table[0].long()].cpu().transpose(1, 2).reshape(-1, hkv, d + 16)[:T], rec)
+    assert int(kv[:470_000].count_nonzero()) == 0
+    rk, rv, _ = R.values(rec)
+    k16, v16 = sa.expand_kv4(c, table[0], ws=ws)
+    assert torch.equal(k16.cpu().transpose(1, 2).reshape(-1, hkv, d)[:T], rk.bfloat16())
+    small = kv[table[0].long()].cpu()
+    blocks, cnt = R.pack_entries([R.entries_of([(0, T)], T, page)])
+    ql = q[-1:].contiguous()
+    ref = R.decode(small, torch.tensor([[0, 1, 2]]), ql.cpu(), lambda b, h: torch.arange(T), 0.1)
+    idx = torch.arange(T).int().view(1, 1, T).to(cuda_dev)
+    for sel in (sa.BlockSelection(blocks.to(cuda_dev), cnt.to(cuda_dev)),
+                sa.TokenSelection(idx, torch.full((1, 1), T, dtype=torch.int32, device=cuda_dev))):
+        R.check_decode(sa.sparse_decode_attn(c, ql, sel, 0.1, ws=ws), ref)
+    del kv, c
+    kp = torch.zeros(300_000, hkv, page, d, dtype=torch.bfloat16, device=cuda_dev)   # 4.9 GB
+    vp = torch.zeros_like(kp)
+    top = torch.tensor([299_999, 280_001, 290_003], dtype=torch.int64)
+    slots = (top[torch.arange(T) // page] * page + torch.arange(T) % page).to(cuda_dev)
+    c = sa.PagedCache(kp, vp, table, lens)
+    sa.rope_append(c, xd[:, :1], xd[:, 1:2], xd[:, 2:], pos.to(cuda_dev), slots, ws=ws)
+    for pool, row in ((kp, 1), (vp, 2)):
+        got = pool[top.to(cuda_dev)].transpose(1, 2).reshape(-1, hkv, d)[:T]
+        assert torch.equal(got, xd[:, row:row + 1]) and int(pool[:280_000].count_nonzero()) == 0
+    ws.raise_on_fault("past 32 bits")
+
+
 @pytest.mark.parametrize("splits", [1, 3])
 def test_value_scales_far_apart(cuda_dev, splits):
     """Value rows from 2^-40 to 2^20 of one another, rising, falling and mixed, with

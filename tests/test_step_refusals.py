@@ -220,6 +220,10 @@ def test_binding_refusals():
                        plan=sa.AppendPlan.empty(2, 5, "cpu"))
     with pytest.raises(sa.SAError):      # top-k reads bf16 pages
         sa.workspace_bytes(L.OP_SELECT_TOPK, c, num_q_heads=4, k=8)
+    with pytest.raises(TypeError, match="expand_kv4"):
+        sa.select_topk(c, q[:2], 4)
+    with pytest.raises(TypeError, match="expand_kv4"):
+        sa.select_blocks_rbs(c, q)
 
 
 def test_rows_layouts():
