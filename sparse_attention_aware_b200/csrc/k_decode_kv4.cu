@@ -759,25 +759,42 @@ __global__ void __launch_bounds__(128) k_kv4_combine(const DecodeArgs a, int row
     const size_t row = r;
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + row * a.S;
     const float *po = a.part_o + row * a.S * D + c;
-    float M = -INFINITY;
-#pragma unroll 4
-    for (int s = 0; s < a.S; ++s) {
-        const float2 x = ml[s];
-        if (x.y != 0.f) M = fmaxf(M, x.x);
-    }
+    // 8 splits at a time, states and outputs in one trip (an empty split's output
+    // is whatever the workspace held, and is not looked at)
+    float M = -INFINITY, Ls = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    float Ls = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < a.S; ++s) {
-        const float2 x = ml[s];
-        if (x.y == 0.f) continue;
-        const float w = ex2(x.x - M);
-        const float4 v = *reinterpret_cast<const float4 *>(po + (size_t)s * D);
-        Ls = fmaf(w, x.y, Ls);
-        O.x = fmaf(w, v.x, O.x);
-        O.y = fmaf(w, v.y, O.y);
-        O.z = fmaf(w, v.z, O.z);
-        O.w = fmaf(w, v.w, O.w);
+    for (int s0 = 0; s0 < a.S; s0 += 8) {
+        float2 x[8];
+        float4 v[8];
+        float top = M;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            x[u] = make_float2(-INFINITY, 0.f);
+            if (s0 + u < a.S) {
+                x[u] = ml[s0 + u];
+                v[u] = *reinterpret_cast<const float4 *>(po + (size_t)(s0 + u) * D);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (x[u].y != 0.f) top = fmaxf(top, x[u].x);
+        const float al = top == M ? 1.f : ex2(M - top);
+        M = top;
+        Ls *= al;
+        O.x *= al;
+        O.y *= al;
+        O.z *= al;
+        O.w *= al;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (x[u].y == 0.f) continue;
+            const float w = ex2(x[u].x - M);
+            Ls = fmaf(w, x[u].y, Ls);
+            O.x = fmaf(w, v[u].x, O.x);
+            O.y = fmaf(w, v[u].y, O.y);
+            O.z = fmaf(w, v[u].z, O.z);
+            O.w = fmaf(w, v[u].w, O.w);
+        }
     }
     finish(a, row, D, c, M, Ls, O);
 }
