@@ -147,7 +147,7 @@ __device__ __forceinline__ void quantize_row(const double (&y)[8], uint32_t &cod
         lo = l < lo ? l : lo;
         hi = h > hi ? h : hi;
     }
-    const unsigned half_lanes = ((1u << HL) - 1) << ((threadIdx.x) & ~(HL - 1));
+    const unsigned half_lanes = ((1u << HL) - 1) << (threadIdx.x & ~(HL - 1));
     const unsigned finite = __ballot_sync(~0u, fine);
     const __nv_bfloat16 zb = __float2bfloat16_rn((float)lo), sb = __float2bfloat16_rn((float)((hi - lo) / 15.0));
     const float zf = __bfloat162float(zb), sf = __bfloat162float(sb);
@@ -234,29 +234,25 @@ __device__ __forceinline__ bool quantize_row32(const float (&y)[8], const float 
 {
     constexpr int HL = D / 16;               // lanes of a half
     constexpr float MAGIC = 12582912.f;      // 1.5 * 2^23: x + MAGIC holds the nearest whole number in its low bits
-    float lo = y[0], hi = y[0], nan = 0.f;   // nan: not a number if an element is not finite
+    float lo = y[0], hi = y[0];   // (a NaN is passed over here and fails the test of its code)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 1; e < 8; ++e) {
         lo = fminf(lo, y[e]);
         hi = fmaxf(hi, y[e]);
-        nan = fmaf(y[e], 0.f, nan);
     }
 #pragma unroll
     for (int o = HL / 2; o > 0; o >>= 1) {
         lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
     }
-    const unsigned half_lanes = ((1u << HL) - 1) << ((threadIdx.x) & ~(HL - 1));
-    const unsigned finite = __ballot_sync(~0u, nan == 0.f);
     const float top = fmaxf(fabsf(lo), fabsf(hi));
     const float err = exact ? 0.f : fmaxf(top, __shfl_xor_sync(~0u, top, HL)) * (36.f / 16777216.f);   // of the row
     auto bf = [](float x) { return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x)); };
     const float range = (hi - lo) * (1.f / 15.f), slack = fmaf(range, 4.8e-7f, 0.25f * err);   // 8 u, and 2 err / 15
     const uint32_t zb = bf(lo - err), sb = bf(range - slack);
     const float z = bf_lo(zb), s = bf_lo(sb);
-    // (subnormal or huge rows are left to fp64)
-    bool sure = zb == bf(lo + err) && sb == bf(range + slack) && (finite & half_lanes) == half_lanes && s > 1e-30f &&
-                top < 1e30f;
+    // (subnormal, huge and infinite rows are left to fp64)
+    bool sure = zb == bf(lo + err) && sb == bf(range + slack) && s > 1e-30f && top < 1e30f;
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));   // within 1 ulp
     // quotients y / s - z / s: each product and the quotient's reciprocal are within 4 u
