@@ -483,13 +483,15 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t s)
     if (a.T == 0) return cudaSuccess;
     const int rpw = 256 / a.D;
     const int tasks = (a.Hq + rpw - 1) / rpw + 2 * ((a.Hkv + rpw - 1) / rpw);
-    // a warp per token, or more while that leaves the device short of warps
-    // (32 an SM, twice): one token's heads are then taken at once
-    long long wpt = (2 * 148 * 32 + a.T - 1) / a.T;
+    // a warp per token, or more up to 16 warps an SM: a token's heads are then
+    // taken at once, at the price of its angles in each warp (512 and 2048 tokens
+    // of 32 + 2 x 8 heads into bf16 pages: with 64 warps an SM 10.4 and 17.5 us,
+    // 32: 7.3 and 16.1, 16: 6.5 and 13.2, 8: 5.8 and 15.7, 4: 6.3 and 15.7)
+    long long wpt = (16 * 148 + a.T - 1) / a.T;
     // (a warp keeps marks of up to 64 tasks of keys and values)
     const int least = (a.Hkv + 32 * rpw - 1) / (32 * rpw);
     wpt = wpt < least ? least : wpt > tasks ? tasks : wpt;
-    const dim3 grid((unsigned)(wpt * a.T));   // at most max(a.T, 9472 + a.T, least a.T) blocks
+    const dim3 grid((unsigned)(wpt * a.T));   // at most max(2368 + a.T, least a.T) blocks
     auto kern = a.kv4 ? (a.D == 64 ? k_rope_append<64, 4> : k_rope_append<128, 4>)
                       : (a.D == 64 ? k_rope_append<64, 16> : k_rope_append<128, 16>);
     return launch_pdl(kern, grid, dim3(kAppendThreads), 0, s, a, (int)wpt);

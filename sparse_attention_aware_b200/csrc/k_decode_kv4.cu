@@ -72,7 +72,7 @@ constexpr int kDW = 4;                   // warps per CTA
 constexpr int kDThreads = kDW * 32;
 constexpr int kDR = 32;                  // rows per stage (two of the MMA's M)
 constexpr int kDST = 3;                   // ring stages per warp
-constexpr int kLeast = 256, kLong = 1024;   // tokens of a split: see split_at
+constexpr int kLeast = 256;              // tokens of a split at least
 constexpr float kLazy = 8.f;             // log2 of how far a score may pass the running maximum
 
 template <int D>
@@ -178,20 +178,21 @@ __device__ __forceinline__ void query8(const void *q, size_t i, float (&x)[8])
 }
 
 // Where split s of a list of n begins, in units of `unit` positions.  The list
-// is cut into at most S splits of at least `least`.  Long splits (`long_` and
-// more) are cut at n (1 - (1 - s/S)^2), each smaller than the one before it:
-// CTAs are launched in order of s, so the long splits of all sequences go
-// first and the short ones fill the device's slots as they fall free (equal
-// splits left 16% of it idle at the end of a launch of ragged sequences).
-// Short ones are equal: all run at once, and the longest sets the time.
-__device__ __forceinline__ int split_at(int n, int s, int S, int least, int long_, int unit)
+// is cut into at most S splits of at least `least`.  Where the launch has more
+// CTAs than run at once (`guided`) the cuts are at n (1 - (1 - s/S)^2), each
+// split smaller than the one before it: CTAs are launched in order of s, so the
+// long splits of all sequences go first and the short ones fill the device's
+// slots as they fall free (equal splits left 16% of it idle at the end of a
+// launch of ragged sequences).  Where all run at once the longest sets the time,
+// and splits are equal.
+__device__ __forceinline__ int split_at(int n, int s, int S, int least, bool guided, int unit)
 {
     S = min(S, (n + least - 1) / least);
     if (s <= 0) return 0;
     if (s >= S) return n;
     // (fp32: only the order of the boundaries matters, and rounding keeps it)
     float left = (float)(S - s) / (float)S;
-    if (n >= long_ * S) left *= left;
+    if (guided) left *= left;
     return n - min(n, ((int)((float)n * left) + unit - 1) & ~(unit - 1));
 }
 
@@ -206,10 +207,14 @@ __device__ __forceinline__ void finish(const DecodeArgs &a, size_t row, int D, i
     if (a.lse && c == 0) a.lse[row] = some ? (M + log2f(Ls)) * kLn2 : -INFINITY;
 }
 
+// CTAs an SM holds (by registers; 4 of the token lists' fit with 128)
+template <int NH, bool QF32, bool TOKENS>
+constexpr int kOcc = NH == 1 ? (TOKENS && !QF32 ? 4 : 3) : 2;
+
 // NH = 8-head column blocks of the CTA (1 or 2); TOKENS: one query head and
 // its token list, else a kv head's heads and the sequence's block list
 template <int D, int NH, bool QF32, bool TOKENS>
-__global__ void __launch_bounds__(kDThreads, NH == 1 ? (TOKENS && !QF32 ? 4 : 3) : 2) k_decode_kv4(const DecodeArgs a)
+__global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv4(const DecodeArgs a)
 {
     pdl_wait();
     pdl_trigger();
@@ -253,6 +258,7 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? (TOKENS && !QF32 ? 4 : 3)
         if (reports) fault(st, CHK_SEQ_LEN, L);
         L = L < 0 ? 0 : Lcap;
     }
+    const bool guided = (unsigned long long)gridDim.x * gridDim.y * gridDim.z > 148 * kOcc<NH, QF32, TOKENS>;
     // this split's range [lo, hi) of list positions (tokens) or entries (blocks)
     int lo, hi;
     const int *pt = a.c.pt + (size_t)b * a.c.max_pages;
@@ -265,16 +271,16 @@ __global__ void __launch_bounds__(kDThreads, NH == 1 ? (TOKENS && !QF32 ? 4 : 3)
             n = n < 0 ? 0 : a.kcap;
         }
         idx = a.idx + r * a.kcap;
-        lo = split_at(n, s, a.S, kLeast, kLong, kDR);
-        hi = split_at(n, s + 1, a.S, kLeast, kLong, kDR);
+        lo = split_at(n, s, a.S, kLeast, guided, kDR);
+        hi = split_at(n, s + 1, a.S, kLeast, guided, kDR);
     } else {
         if (n < 0 || n > a.max_blocks) {
             if (reports) fault(st, CHK_BLOCK_ENTRY, n);
             n = n < 0 ? 0 : a.max_blocks;
         }
         ent = reinterpret_cast<const int4 *>(a.ent) + (size_t)b * a.max_blocks;
-        lo = split_at(n, s, a.S, kLeast >> a.c.Plog2, kLong >> a.c.Plog2, 1);
-        hi = split_at(n, s + 1, a.S, kLeast >> a.c.Plog2, kLong >> a.c.Plog2, 1);
+        lo = split_at(n, s, a.S, kLeast >> a.c.Plog2, guided, 1);
+        hi = split_at(n, s + 1, a.S, kLeast >> a.c.Plog2, guided, 1);
     }
     // what this CTA has of 4 columns of an output row: the output itself where there
     // is one split, else a part for the combine kernel
@@ -822,18 +828,42 @@ cudaError_t launch_kind(const DecodeArgs &a, cudaStream_t s)
 
 }  // namespace
 
-// Enough CTAs to fill the device (3 an SM) between two and three times over,
-// but no split below 512 tokens of the longest possible list: at 32 x 8 groups
-// of up to 16384 tokens 3, 4, 5 and 8 splits take 105, 95, 94 and 99 us, at 32
-// x 32 lists of 4096 tokens 1, 2 and 3 take 167, 150 and 158 us, and at 4 x 8
-// lists of up to 4096 tokens (one wave of CTAs) 4, 8 and 16 take 17, 12 and 13.
-int decode_kv4_splits(int B, int rows, long long list)
+// The split count that a simple model of the launch finds fastest.  A CTA costs
+// kStart beside `each` a token when its SM is full, less when it is not; CTAs
+// that all run at once take as long as one of them, more of them fill the slots
+// with falling sizes (split_at), the first of which must fit in as well, and
+// leave a tail.  The constants are measured ones (us) for head_dim 128:
+//   32 x 8 groups of up to 16384 tokens  3, 4, 5, 8 splits  101, 93, 92, 96 us
+//   32 x 32 lists of 4096 tokens         1, 2, 3 splits     160, 144, 154 us
+//   8 x 32 lists of 2048 tokens          1, 2, 4 splits     37, 29, 28 us
+//   1 x 8 groups of 131072 tokens        24, 37, 55, 64     56, 41, 41, 47 us
+//   4 x 8 groups of a masked step        4, 8, 13 splits    12.1, 10.4, 12.1 us
+int decode_kv4_splits(int B, int rows, long long list, int D, bool tokens, bool f32, bool wide)
 {
-    const long long units = (long long)B * rows;
-    if (units <= 0) return 1;
-    const long long want = (2 * 148 * 4 + units - 1) / units, most = (list + 511) / 512;
-    const long long s = want < most ? want : most;
-    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+    const double units = (double)B * rows, start = 4.0;
+    if (units <= 0 || list <= 0) return 1;
+    const double slots = 148.0 * (wide ? 2 : tokens && !f32 ? 4 : 3);
+    const double each = (tokens ? 0.0176 : wide ? 0.016 : 0.0118) * (D + 32) / 160;
+    int best = 1;
+    double least = 0;
+    for (int S = 1; S <= 64; ++S) {
+        const double n = (double)list / S, ctas = units * S;
+        if (S > 1 && n < kLeast) break;
+        double t;
+        if (ctas <= slots) {
+            t = start + each * n * (0.4 + 0.6 * ctas / slots);
+        } else {
+            const double first = start + each * list * (2.0 * S - 1) / ((double)S * S);
+            t = (ctas * start + units * list * each) / slots;
+            t = (t > first ? t : first) + start + each * n / 2;
+        }
+        if (S > 1) t += 1.2 + (S + 7) / 8;   // the combine: a trip to memory for 8 splits
+        if (S == 1 || t < least) {
+            least = t;
+            best = S;
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_decode_kv4(const DecodeArgs &a, cudaStream_t s)

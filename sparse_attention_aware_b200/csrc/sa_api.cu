@@ -87,6 +87,15 @@ sa_status check_cache4(const sa_kv4_cache *kv, CacheArgs *c)
 // CTAs per (sequence, split) of a block-list decode over a 4-bit cache
 int kv4_group_rows(const sa_kv4_cache *kv, int Hq) { return kv->num_kv_heads * ((Hq / kv->num_kv_heads + 15) / 16); }
 
+// Most splits that are chosen for a caller: 2400 CTAs of groups, which is past
+// where more splits help, so that the workspace stays in proportion
+int kv4_most_splits(const sa_kv4_cache *kv, int Hq)
+{
+    const long long units = (long long)kv->batch * kv4_group_rows(kv, Hq);
+    const long long s = units > 0 ? (2400 + units - 1) / units : 1;
+    return (int)(s > 64 ? 64 : s < 1 ? 1 : s);
+}
+
 // Fields of a decode that both cache kinds share, checked and set.
 sa_status check_decode(int B, int Hkv, const void *q, sa_dtype q_dtype, int Hq, const sa_selection *sel, float scale,
                        const void *out, const float *lse, DecodeArgs *a)
@@ -598,7 +607,8 @@ size_t sa_kv4_decode_workspace_bytes(const sa_kv4_cache *kv, int32_t num_q_heads
     sa_kv_cache as{};
     as.batch = kv->batch;
     as.head_dim = kv->head_dim;
-    const int most = num_splits > 0 ? num_splits : decode_kv4_splits(kv->batch, kv4_group_rows(kv, num_q_heads), 1LL << 31);
+    // (chosen splits: no more CTAs than make the partial states worth their bytes)
+    const int most = num_splits > 0 ? num_splits : kv4_most_splits(kv, num_q_heads);
     return sa::decode_workspace_bytes(&as, num_q_heads, most);
 }
 
@@ -616,10 +626,12 @@ sa_status sa_sparse_decode_attn_kv4(const sa_kv4_cache *kv, const void *q, sa_dt
     st = check_ws(ws, ws_bytes, sa_kv4_decode_workspace_bytes(kv, num_q_heads, num_splits));
     if (st != SA_OK) return st;
     if (num_splits == 0) {
-        // (a token list has a CTA per query head, so never more splits than the workspace was sized for)
-        num_splits = a.blocks ? decode_kv4_splits(kv->batch, kv4_group_rows(kv, num_q_heads),
-                                                  (long long)a.max_blocks * kv->page_size)
-                              : decode_kv4_splits(kv->batch, num_q_heads, a.kcap);
+        const bool wide = a.blocks && num_q_heads / kv->num_kv_heads > 8;
+        num_splits = decode_kv4_splits(kv->batch, a.blocks ? kv4_group_rows(kv, num_q_heads) : num_q_heads,
+                                       a.blocks ? (long long)a.max_blocks * kv->page_size : (long long)a.kcap,
+                                       kv->head_dim, !a.blocks, a.q_f32, wide);
+        const int most = kv4_most_splits(kv, num_q_heads);
+        if (num_splits > most) num_splits = most;
     }
     char *w = static_cast<char *>(ws);
     const size_t rows = (size_t)kv->batch * num_q_heads;

@@ -60,8 +60,9 @@ bool decode_gqa_supported(const DecodeArgs &a);
 cudaError_t launch_decode_gqa_split(const DecodeArgs &a, cudaStream_t s);
 // decode over a 4-bit cache (k_decode_kv4.cu): a.c.k holds the records
 cudaError_t launch_decode_kv4(const DecodeArgs &a, cudaStream_t s);
-// its split count for `rows` CTAs per (sequence, split) and lists of up to `list` tokens
-int decode_kv4_splits(int B, int rows, long long list);
+// its split count for `rows` CTAs per (sequence, split) and lists of up to `list` tokens (wide: more than 8 query
+// heads a CTA)
+int decode_kv4_splits(int B, int rows, long long list, int D, bool tokens, bool f32, bool wide);
 
 // ---- top-k ------------------------------------------------------------------
 struct TopkArgs {
