@@ -212,8 +212,10 @@ template <int NH, bool QF32, bool TOKENS>
 constexpr int kOcc = NH == 1 ? (TOKENS && !QF32 ? 4 : 3) : 2;
 
 // NH = 8-head column blocks of the CTA (1 or 2); TOKENS: one query head and
-// its token list, else a kv head's heads and the sequence's block list
-template <int D, int NH, bool QF32, bool TOKENS>
+// its token list, else a kv head's heads and the sequence's block list; PACK: at
+// most 4 heads, which stand in columns 0-3 for one 16-row tile and again in 4-7
+// for the other, so that the softmax of both fills the 8 columns
+template <int D, int NH, bool QF32, bool TOKENS, bool PACK>
 __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv4(const DecodeArgs a)
 {
     pdl_wait();
@@ -224,11 +226,13 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
     constexpr int CBH = CB / 2;          // of a half
     constexpr int TT = NH == 1 ? 2 : 1;  // 16-row tiles at a time
     constexpr int NQ = QF32 ? 2 : 1;     // fp16 parts of the query
+    constexpr int TS = PACK ? 1 : TT;    // tiles whose softmax a lane does
     extern __shared__ __align__(128) uint8_t sm[];
     const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(sm);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gq = lane >> 2, tq = lane & 3;   // mma group id / thread in group
+    const int own = PACK ? tq >> 1 : 0;        // PACK: the tile whose scores are in this lane's columns
     const int s = blockIdx.z, b = blockIdx.y;
     const int HPG = a.Hq / a.c.Hkv;
     const int hblocks = (HPG + 15) / 16;
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
     float qx[NH][CB][8];
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
-        const int h = nh * 8 + gq;
+        const int h = nh * 8 + (PACK ? gq & 3 : gq);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
 #pragma unroll
@@ -381,13 +385,14 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
         const bool partial = mask != (TT == 2 ? 0xffffffffu : 0xffffu);
         // scales and zeros {K half 0, K half 1, V half 0, V half 1} of rows gq, gq + 8; a row
         // outside the mask is whatever the stage held, and must not reach a product
-        uint4 par[TT][2];
+        uint4 par[TS][2];
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+        for (int t = 0; t < TS; ++t)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                par[t][r] = *reinterpret_cast<const uint4 *>(ring + at + (t * 16 + r * 8 + gq) * REC + Kv4<D>::PAR);
-                if (partial && !((mask >> (t * 16 + r * 8 + gq)) & 1)) par[t][r] = make_uint4(0, 0, 0, 0);
+                const int row = (t + own) * 16 + r * 8 + gq;
+                par[t][r] = *reinterpret_cast<const uint4 *>(ring + at + row * REC + Kv4<D>::PAR);
+                if (partial && !((mask >> row) & 1)) par[t][r] = make_uint4(0, 0, 0, 0);
             }
 
         // ---- S^T = K Q^T per half
@@ -420,10 +425,16 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
                             }
                 }
             }
-        // ---- scores: rows gq (elements 0, 1) and gq + 8 (2, 3), base-2 domain
-        float x[TT][NH][4], above = -INFINITY, vs[2] = {0.f, 0.f};
+        if (PACK) {
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[0][half][0][i] = own ? sc[TT - 1][half][0][i] : sc[0][half][0][i];
+        }
+        // ---- scores: rows gq (elements 0, 1) and gq + 8 (2, 3), base-2 domain
+        float x[TS][NH][4], above = -INFINITY, vs[2] = {0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < TS; ++t)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const uint4 &p = par[t][r];
@@ -441,10 +452,10 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
             }
         if (partial) {
 #pragma unroll
-            for (int t = 0; t < TT; ++t)
+            for (int t = 0; t < TS; ++t)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    if (!((mask >> (t * 16 + r * 8 + gq)) & 1)) {
+                    if (!((mask >> ((t + own) * 16 + r * 8 + gq)) & 1)) {
 #pragma unroll
                         for (int nh = 0; nh < NH; ++nh) x[t][nh][2 * r] = x[t][nh][2 * r + 1] = -INFINITY;
                     }
@@ -457,7 +468,7 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 top[nh][j] = fmaxf(x[0][nh][j], x[0][nh][2 + j]);
-                if (TT == 2) top[nh][j] = fmaxf(top[nh][j], fmaxf(x[TT - 1][nh][j], x[TT - 1][nh][2 + j]));
+                if (TS == 2) top[nh][j] = fmaxf(top[nh][j], fmaxf(x[TS - 1][nh][j], x[TS - 1][nh][2 + j]));
                 above = fmaxf(above, top[nh][j] - mh[nh][j]);
             }
         if (__any_sync(~0u, above > kLazy || vs[0] > smax[0] || vs[1] > smax[1])) {
@@ -500,7 +511,7 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
         // ---- weights; P'^T (tokens x heads) per half as B fragments (k = tokens)
         uint32_t pb[TT][2][NH][2];
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+        for (int t = 0; t < TS; ++t)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const uint4 &pr = par[t][r];
@@ -521,6 +532,15 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
                     pb[t][1][nh][r] = movm(pack_pair(p[0] * w1, p[1] * w1));
                 }
             }
+        if (PACK) {   // each tile's own columns
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    pb[TT - 1][half][0][r] = gq < 4 ? 0u : pb[0][half][0][r];
+                    pb[0][half][0][r] = gq < 4 ? pb[0][half][0][r] : 0u;
+                }
+        }
         // ---- O^T += V^T P'^T: transposed 8x8 loads of the code bytes give, per
         // register, 4 channels of tokens 2tq (low half) and 2tq + 1 (high half)
 #pragma unroll
@@ -701,8 +721,8 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
     float *mo = reinterpret_cast<float *>(sm);                 // [warp][16][ROW]
     float *mm = mo + kDW * 16 * ROW;                            // [warp][16]
     float *ml = mm + kDW * 16;                                  // [warp][16]
-    // (a token list has one head, column 0)
-    if (!TOKENS || tq == 0) {
+    // (a token list has one head, columns 0 and 4)
+    if (!TOKENS || (tq & 1) == 0) {
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
@@ -729,17 +749,19 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
     __syncthreads();
     for (int i = tid; i < nheads * (D / 4); i += kDThreads) {
         const int j = i / (D / 4), c = i % (D / 4) * 4;
+        constexpr int PARTS = PACK ? 2 : 1;   // columns of a head
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kDW; ++w) M = fmaxf(M, mm[w * 16 + j]);
+        for (int w = 0; w < kDW * PARTS; ++w) M = fmaxf(M, mm[w / PARTS * 16 + w % PARTS * 4 + j]);
         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
         float Ls = 0.f;
 #pragma unroll
-        for (int w = 0; w < kDW; ++w) {
-            const float lw = ml[w * 16 + j];
+        for (int w = 0; w < kDW * PARTS; ++w) {
+            const int at = w / PARTS * 16 + w % PARTS * 4 + j;
+            const float lw = ml[at];
             if (lw == 0.f) continue;   // no token (a sum that is not a number is taken along)
-            const float wgt = ex2(mm[w * 16 + j] - M);
-            const float4 x = *reinterpret_cast<const float4 *>(mo + (w * 16 + j) * ROW + c);
+            const float wgt = ex2(mm[at] - M);
+            const float4 x = *reinterpret_cast<const float4 *>(mo + at * ROW + c);
             O.x = fmaf(wgt, x.x, O.x);
             O.y = fmaf(wgt, x.y, O.y);
             O.z = fmaf(wgt, x.z, O.z);
@@ -805,11 +827,11 @@ __global__ void __launch_bounds__(128) k_kv4_combine(const DecodeArgs a, int row
     finish(a, row, D, c, M, Ls, O);
 }
 
-template <int D, int NH, bool QF32, bool TOKENS>
+template <int D, int NH, bool QF32, bool TOKENS, bool PACK>
 cudaError_t launch_kv4(const DecodeArgs &a, cudaStream_t s)
 {
     constexpr int smem = DSmem<D>::BYTES;
-    auto kern = k_decode_kv4<D, NH, QF32, TOKENS>;
+    auto kern = k_decode_kv4<D, NH, QF32, TOKENS, PACK>;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
     const int hpg = a.Hq / a.c.Hkv;
     const dim3 grid((unsigned)(TOKENS ? a.Hq : a.c.Hkv * ((hpg + 15) / 16)), (unsigned)a.c.B, (unsigned)a.S);
@@ -822,8 +844,11 @@ cudaError_t launch_kv4(const DecodeArgs &a, cudaStream_t s)
 template <int D, bool QF32>
 cudaError_t launch_kind(const DecodeArgs &a, cudaStream_t s)
 {
-    if (!a.blocks) return launch_kv4<D, 1, QF32, true>(a, s);
-    return a.Hq / a.c.Hkv <= 8 ? launch_kv4<D, 1, QF32, false>(a, s) : launch_kv4<D, 2, QF32, false>(a, s);
+    if (!a.blocks) return launch_kv4<D, 1, QF32, true, true>(a, s);
+    const int hpg = a.Hq / a.c.Hkv;
+    return hpg <= 4   ? launch_kv4<D, 1, QF32, false, true>(a, s)
+           : hpg <= 8 ? launch_kv4<D, 1, QF32, false, false>(a, s)
+                      : launch_kv4<D, 2, QF32, false, false>(a, s);
 }
 
 }  // namespace
