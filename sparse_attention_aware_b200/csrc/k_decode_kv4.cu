@@ -149,6 +149,16 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t (&f)[4])
     f[2] = x & 0x000f000fu;
     f[3] = x & 0x00f000f0u;
 }
+// the same for sums from which the even codes can be taken out afterwards: f[i]
+// holds c 2^-24 for even i, for odd i the byte (16 c + the even code before it)
+// 2^-24, which needs no mask of its own
+__device__ __forceinline__ void widen_bytes(uint32_t w, uint32_t (&f)[4])
+{
+    f[1] = w & 0x00ff00ffu;
+    f[3] = __byte_perm(w, 0u, 0x4341);
+    f[0] = w & 0x000f000fu;
+    f[2] = f[3] & 0x000f000fu;
+}
 constexpr uint32_t kOnes = 0x3c003c00u, kSixteens = 0x4c004c00u;   // fp16 pairs
 
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi)
@@ -552,8 +562,8 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     uint32_t f0[4], f1[4];
-                    widen(w[2 * u], f0);
-                    widen(w[2 * u + 1], f1);
+                    widen_bytes(w[2 * u], f0);
+                    widen_bytes(w[2 * u + 1], f1);
                     const int cb = c2 + u, half = cb / CBH;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
@@ -729,12 +739,13 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
             for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
                 for (int i = 0; i < (TOKENS ? 1 : 2); ++i) {
-                    // channels 4gq .. 4gq + 3 of block cb; the odd ones (rows gq + 8) went in as 16 c
+                    // channels 4gq .. 4gq + 3 of block cb; the odd ones (rows gq + 8) went in as
+                    // 16 c and the even one's code
                     const int half = cb / CBH;
                     const float f = 16777216.f / keep[half], odd = f * 0.0625f, z = zs[half][nh][i];
                     *reinterpret_cast<float4 *>(mo + (warp * 16 + nh * 8 + 2 * tq + i) * ROW + cb * 32 + 4 * gq) =
-                        make_float4(fmaf(o[cb][0][nh][i], f, z), fmaf(o[cb][0][nh][2 + i], odd, z),
-                                    fmaf(o[cb][1][nh][i], f, z), fmaf(o[cb][1][nh][2 + i], odd, z));
+                        make_float4(fmaf(o[cb][0][nh][i], f, z), fmaf(o[cb][0][nh][2 + i] - o[cb][0][nh][i], odd, z),
+                                    fmaf(o[cb][1][nh][i], f, z), fmaf(o[cb][1][nh][2 + i] - o[cb][1][nh][i], odd, z));
                 }
     }
     if (gq == 0) {
