@@ -865,21 +865,26 @@ cudaError_t launch_kind(const DecodeArgs &a, cudaStream_t s)
 }  // namespace
 
 // The split count that a simple model of the launch finds fastest.  A CTA costs
-// kStart beside `each` a token when its SM is full, less when it is not; CTAs
-// that all run at once take as long as one of them, more of them fill the slots
-// with falling sizes (split_at), the first of which must fit in as well, and
-// leave a tail.  The constants are measured ones (us) for head_dim 128:
-//   32 x 8 groups of up to 16384 tokens  3, 4, 5, 8 splits  101, 93, 92, 96 us
-//   32 x 32 lists of 4096 tokens         1, 2, 3 splits     160, 144, 154 us
-//   8 x 32 lists of 2048 tokens          1, 2, 4 splits     37, 29, 28 us
-//   1 x 8 groups of 131072 tokens        24, 37, 55, 64     56, 41, 41, 47 us
-//   4 x 8 groups of a masked step        4, 8, 13 splits    12.1, 10.4, 12.1 us
+// `start` beside `each` a token when its SM is full, less when it is not; CTAs
+// that all run at once take as long as one of the longest row, more of them fill
+// the slots with falling sizes (split_at), the first of which must fit in as well,
+// and leave a tail.  The sequences of a batch differ, so their block lists are taken
+// to hold 0.72 of the longest one's entries on average (lengths spread over a factor
+// of 2).  The constants are fitted to measured times (us, head_dim 128):
+//   32 x 8 groups of up to 16384 tokens  3, 4, 5, 6, 8 splits   87, 81, 80, 80, 83
+//   16 x 8 (8 heads each)                3, 4, 6, 8, 10, 16     64, 69, 54, 51, 52, 57
+//   64 x 8 groups of up to 4096          1, 2, 3, 4             57, 50, 53, 56
+//   1 x 8 groups of 131072 tokens        24, 37, 55, 64         41, 37, 37, 42
+//   4 x 8 groups of a masked step        4, 8, 13               11.5, 9.9, 11.4
+//   32 x 32 lists of 4096 tokens         1, 2, 3, 4             150, 141, 144, 151
+//   8 x 32 lists of 2048 tokens          1, 2, 3, 4             34, 27, 26, 27
 int decode_kv4_splits(int B, int rows, long long list, int D, bool tokens, bool f32, bool wide)
 {
     const double units = (double)B * rows, start = 4.0;
     if (units <= 0 || list <= 0) return 1;
     const double slots = 148.0 * (wide ? 2 : tokens && !f32 ? 4 : 3);
-    const double each = (tokens ? 0.0176 : wide ? 0.016 : 0.0118) * (D + 32) / 160;
+    const double each = (tokens ? 0.0176 : wide ? 0.013 : 0.0095) * (D + 32) / 160;
+    const double filled = tokens || B == 1 ? 1.0 : 0.72;
     int best = 1;
     double least = 0;
     for (int S = 1; S <= 64; ++S) {
@@ -887,11 +892,11 @@ int decode_kv4_splits(int B, int rows, long long list, int D, bool tokens, bool 
         if (S > 1 && n < kLeast) break;
         double t;
         if (ctas <= slots) {
-            t = start + each * n * (0.4 + 0.6 * ctas / slots);
+            t = start + each * n * (0.3 + 0.7 * ctas / slots);
         } else {
             const double first = start + each * list * (2.0 * S - 1) / ((double)S * S);
-            t = (ctas * start + units * list * each) / slots;
-            t = (t > first ? t : first) + start + each * n / 2;
+            t = (ctas * start + filled * units * list * each) / slots;
+            t = (t > first ? t : first) + start + each * n / (2 * S);
         }
         if (S > 1) t += 1.2 + (S + 7) / 8;   // the combine: a trip to memory for 8 splits
         if (S == 1 || t < least) {
