@@ -17,7 +17,7 @@
 // warp one of whose rows has a code, scale or zero nearer to a border than that
 // (about one in thirty with keys) computes it again in fp64.  (A code next to a
 // border would otherwise come out a full step off; with all keys and values in
-// fp64 the kernel took 237 us for 16391 tokens of 32 + 2 x 8 heads, now 106.)
+// fp64 the kernel took 237 us for 16391 tokens of 32 + 2 x 8 heads, now 104.)
 //
 // Angles are formed in fp64 (position * inv_freq is exact below 2^29),
 // reduced by 2 pi in two parts (Cody and Waite) and only then rounded for the
@@ -30,7 +30,7 @@
 // neighbours), so the rotation needs no exchange between lanes.
 //
 // Measured: 32768 tokens of 32 + 2 x 4 heads into bf16 pages 109 us, 671 MB, 0.94
-// of HBM; 16391 tokens into 4-bit pages 106 us, 354 MB, 0.51 of HBM: bound by
+// of HBM; 16391 tokens into 4-bit pages 104 us, 354 MB, 0.52 of HBM: bound by
 // instructions (about 5000 a token, of which 1900 are the queries'); a step's 32
 // tokens 3.1 us, bound by latency.
 #include <cuda_bf16.h>

@@ -51,15 +51,25 @@
 // score passes it by more than 8 in the base-2 domain: weights stay below 2^8,
 // and most tiles need neither the max across lanes nor a rescale.
 //
+// A group of at most 4 heads fills half of the 8 columns, a token list's head one.
+// Two tiles of 16 rows then share a softmax: the heads stand in columns 0-3 for the
+// one and again in 4-7 for the other, as two states that the merge joins; a tile's
+// products see zeros in the other's columns (whole context 90 -> 81 us, token lists
+// 142.5 -> 138).
+//
 // Measured (B200, 6.55 TB/s copy): every page of 32 sequences of up to 16384
-// tokens, 32 heads on 8 kv heads (435 MB) 92 us, 0.72 of HBM; 1024 lists of 4096
-// of 65536 tokens 144 us (0.58 by the rows' own bytes; a row's 144 bytes touch
-// 192 in 64-byte pieces, and by those it is 0.84); a masked step of 4 sequences
-// 12 us, 256 of 4096 tokens of 4 heads 4.7 us.  The copies alone take 70 and 131
-// us, the arithmetic alone 88 and 127: about 290 instructions per 16 rows, of
-// which no part dominates (leaving out the widening, or half of a product, saves
-// 8 us of 92 each), with 12 to 16 warps an SM.  Short calls are bound by the
-// dependent trips length -> entry -> page -> rows -> merge.
+// tokens, 32 heads on 8 kv heads (435 MB) 80 us, 0.83 of HBM; 1024 lists of 4096
+// of 65536 tokens 138 us (0.60 by the rows' own bytes; a row's 144 bytes touch
+// 192 in 64-byte pieces, and by those it is 0.88); a masked step of 4 sequences
+// 10 us, 256 of 4096 tokens of 4 heads 4.8 us.  The copies alone take 67 and 134
+// us, the arithmetic alone 76 and 123: about 230 instructions per 16 rows (267 with
+// a list), of which widening the codes is a third, with 12 to 16 warps an SM.  Short
+// calls are bound by the dependent trips length -> entry -> page -> rows -> merge.
+//
+// Measured and not kept (whole context, 81 us at that stage): a page segment by
+// bulk copies 88; the next tiles' scores between a tile's weights and its products
+// 80; rings of 4 stages 81; 4 CTAs an SM 82; all rows' entries shared evenly
+// over one wave of CTAs 80, but 53 us and not 50 with 16 sequences of 64/8 heads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
