@@ -445,3 +445,74 @@ def test_a_captured_step_replays(cuda_dev):
     ws.raise_on_fault("graph")
     assert st2[1].tolist() == [steps] * B and torch.equal(st2[3].kv, st[3].kv) and torch.equal(st2[0], st[0])
     del graph
+
+
+@pytest.mark.parametrize("heads,d,page,f32", [(1, 128, 64, False), (2, 64, 16, True), (3, 128, 16, False), (4, 128, 64, False),
+                                              (4, 64, 64, False), (4, 128, 16, True), (5, 128, 64, False), (8, 64, 16, False)])
+@pytest.mark.parametrize("only", ["both", "first", "second", "odd"])
+def test_neighbouring_tiles_of_16_rows_far_apart(cuda_dev, heads, d, page, f32, only):
+    """Every other 16 rows hold keys and values of another size: each head puts its
+    weight on the one kind or the other, and lists may hold one kind alone."""
+    hkv, n = 2, 64 * 21
+    g, kv, table, sl = _cache(31 + heads, 2, hkv, d, page, [n, n - 13])
+    t = torch.arange(n)
+    second = (t // 16 % 2 == 1)
+    for b in range(2):
+        for h in range(hkv):
+            k, v = torch.randn(2, n, d, generator=g).double()
+            k[:, 0] = torch.where(second, -6.0, 6.0).double()
+            v[second] *= 8
+            kv[table[b, t // page].long(), h, t % page] = R.records(k, v)
+    q = torch.randn(2, hkv * heads, d, generator=g)
+    q[:, ::2, 0], q[:, 1::2, 0] = 30.0, -30.0
+    q = q if f32 else q.bfloat16()
+    spans, toks = [], []
+    for m in (n, n - 13):
+        if only == "both":
+            s = [(0, m)]
+        elif only == "odd":
+            s = [(64 * i + 5, min(64 * i + 5 + 11 * (i % 5), m)) for i in range(21) if 64 * i + 5 < m and i % 5]
+        else:
+            s = [(i, min(i + 16, m)) for i in range(16 * (only == "second"), m, 32)]
+        spans.append(s)
+        toks.append(torch.cat([torch.arange(a, e) for a, e in s]))
+    blocks, cnt = R.pack_entries([R.entries_of(s, m, page) for s, m in zip(spans, (n, n - 13))])
+    c = _gpu(kv, table, sl, cuda_dev)
+    ref = R.decode(kv, table, q, lambda b, h: toks[b], 1 / math.sqrt(d))
+    for splits in (0, 1, 3):
+        ws = sa.Workspace(cuda_dev)
+        got = sa.sparse_decode_attn(c, q.to(cuda_dev), sa.BlockSelection(blocks.to(cuda_dev), cnt.to(cuda_dev)),
+                                    1 / math.sqrt(d), splits, ws=ws)
+        assert ws.status()[0] == 0
+        R.check_decode(got, ref, (only, splits))
+    H, most = hkv * heads, max(len(x) for x in toks)
+    idx = torch.full((2, H, most), -1, dtype=torch.int32)
+    for b in range(2):
+        idx[b, :, :len(toks[b])] = toks[b].int()
+    num = torch.tensor([len(x) for x in toks], dtype=torch.int32)[:, None].expand(2, H).contiguous()
+    for splits in (0, 2):
+        R.check_decode(sa.sparse_decode_attn(c, q.to(cuda_dev), sa.TokenSelection(idx.to(cuda_dev), num.to(cuda_dev)),
+                                             1 / math.sqrt(d), splits), ref, (only, "lists", splits))
+
+
+@pytest.mark.parametrize("heads", [2, 8])
+def test_odd_and_even_channels_far_apart(cuda_dev, heads):
+    """Channels at their rows' smallest value beside channels at the largest, odd or
+    even ones: each comes out to its own bf16 rounding (all rows' values are alike)."""
+    d, page, n = 128, 16, 500
+    for low in (0, 1):
+        g, kv, table, sl = _cache(41, 1, 1, d, page, [n])
+        t = torch.arange(n)
+        v = torch.full((n, d), 60.0).double()
+        v[:, low::2] = 0.25
+        kv[table[0, t // page].long(), 0, t % page] = R.records(torch.randn(n, d, generator=g).double(), v)
+        _, rv, _ = R.values(kv[table[0, t // page].long(), 0, t % page])
+        q = torch.randn(1, heads, d, generator=g).bfloat16()
+        blocks, cnt = R.pack_entries([R.entries_of([(0, n)], n, page)])
+        out, _ = sa.sparse_decode_attn(_gpu(kv, table, sl, cuda_dev), q.to(cuda_dev),
+                                       sa.BlockSelection(blocks.to(cuda_dev), cnt.to(cuda_dev)), 0.05)
+        # all rows alike: the output is the row.  A small channel is z p / p beside sums of
+        # codes that cancel exactly (its code is 0); a large one has its weights' 2^-11 and the output's 2^-8
+        want = rv[0].expand(1, heads, d)
+        lim = want.abs() * (R.BF16_HALF + torch.where(torch.arange(d) % 2 == low, 2.0 ** -18, 2.0 ** -10))
+        assert bool(((out.double().cpu() - want).abs() <= lim).all())
