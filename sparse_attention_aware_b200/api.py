@@ -170,8 +170,9 @@ class Workspace:
     to, so the caching allocator does not reuse that memory while a kernel
     launched on one of those streams may still read it."""
 
-    def __init__(self, device=None):
+    def __init__(self, device=None, captured=False):
         self.device = device
+        self._new = torch.empty if captured else torch.zeros   # (of one captured call: its status is not read)
         self.buf: Optional[torch.Tensor] = None
         self._streams = []
         self._raw = {}   # stream handles in _streams -> (aligned address of buf, bytes from there on)
@@ -191,7 +192,7 @@ class Workspace:
         if self.buf is None or self.buf.numel() < nbytes:
             n = max(nbytes, 256)
             old = self.buf
-            self.buf = torch.zeros(n + 256, dtype=torch.uint8, device=self.device or "cuda")
+            self.buf = self._new(n + 256, dtype=torch.uint8, device=self.device or "cuda")
             if old is not None:
                 for s in self._streams:
                     old.record_stream(s)
@@ -395,7 +396,9 @@ def sparse_decode_attn(cache, q: torch.Tensor, sel, scale: Optional[float] = Non
     """Split-KV sparse decode + combine (``sa_sparse_decode_attn``, or
     ``sa_sparse_decode_attn_kv4`` over a PagedCache4).  ``num_splits`` parts a
     list, 1 by default; over a PagedCache4 0, the default there, lets the
-    library choose.  Returns (out bf16, lse fp32)."""
+    library choose.  Captured into a graph without ``ws``, a call over a
+    PagedCache4 keeps its parts in that graph's memory, so that graphs may be
+    replayed side by side.  Returns (out bf16, lse fp32)."""
     if isinstance(cache, PagedCache4):
         return _decode_kv4(cache, q, sel, scale, 0 if num_splits is None else num_splits, out, lse, want_lse, ws, stream)
     if num_splits is None:
@@ -422,7 +425,10 @@ def sparse_decode_attn(cache, q: torch.Tensor, sel, scale: Optional[float] = Non
 
 
 def _decode_kv4(cache: PagedCache4, q, sel, scale, num_splits, out, lse, want_lse, ws, stream):
-    if out is None and lse is None:
+    if ws is None and q.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+        # graphs may be replayed side by side: each call keeps its parts in its graph's own memory
+        ws = Workspace(q.device, captured=True)
+    elif out is None and lse is None:
         way = _short(ws, q.device, stream)
         if way is not None:
             tok = isinstance(sel, TokenSelection)

@@ -516,3 +516,33 @@ def test_odd_and_even_channels_far_apart(cuda_dev, heads):
         want = rv[0].expand(1, heads, d)
         lim = want.abs() * (R.BF16_HALF + torch.where(torch.arange(d) % 2 == low, 2.0 ** -18, 2.0 ** -10))
         assert bool(((out.double().cpu() - want).abs() <= lim).all())
+
+
+def test_graphs_replayed_side_by_side(cuda_dev):
+    """Two graphs captured one after the other without workspaces, replayed on two
+    streams at once: neither's parts reach the other's output."""
+    g, kv, table, sl = _cache(43, 3, 2, 128, 16, [3000, 700, 1999])
+    c = _gpu(kv, table, sl, cuda_dev)
+    blocks, cnt = R.pack_entries([R.entries_of([(0, n)], n, 16) for n in (3000, 700, 1999)])
+    sel = sa.BlockSelection(blocks.to(cuda_dev), cnt.to(cuda_dev))
+    qs = torch.randn(2, 3, 8, 128, generator=g).bfloat16().to(cuda_dev)
+    alone = [sa.sparse_decode_attn(c, q, sel, num_splits=5) for q in qs]
+    torch.cuda.synchronize(cuda_dev)
+    side, graphs, got = torch.cuda.Stream(cuda_dev), [], []
+    with torch.cuda.stream(side):
+        sa.sparse_decode_attn(c, qs[0], sel, num_splits=5)
+    torch.cuda.synchronize(cuda_dev)
+    for q in qs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            for _ in range(20):
+                out = sa.sparse_decode_attn(c, q, sel, num_splits=5)
+        got.append(out)
+    streams = [torch.cuda.Stream(cuda_dev) for _ in range(2)]
+    for _ in range(20):
+        for gr, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                gr.replay()
+        torch.cuda.synchronize(cuda_dev)
+        for a, b in zip(alone, got):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
