@@ -425,10 +425,7 @@ def sparse_decode_attn(cache, q: torch.Tensor, sel, scale: Optional[float] = Non
 
 
 def _decode_kv4(cache: PagedCache4, q, sel, scale, num_splits, out, lse, want_lse, ws, stream):
-    if ws is None and q.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
-        # graphs may be replayed side by side: each call keeps its parts in its graph's own memory
-        ws = Workspace(q.device, captured=True)
-    elif out is None and lse is None:
+    if out is None and lse is None:
         way = _short(ws, q.device, stream)
         if way is not None:
             tok = isinstance(sel, TokenSelection)
@@ -436,7 +433,7 @@ def _decode_kv4(cache: PagedCache4, q, sel, scale, num_splits, out, lse, want_ls
                 fast, wp, wn, raw = way
                 got = fast.decode(cache.kv, cache.page_table, cache.seq_lens, q, sel.idx if tok else sel.blocks,
                                   sel.count if tok else sel.block_counts, L.SEL_TOKENS if tok else L.SEL_BLOCKS, scale,
-                                  num_splits, want_lse, wp, wn, raw)
+                                  num_splits, want_lse, wp, wn, raw, ws is None)
                 if got is not None:
                     if isinstance(got, int):
                         _check(got, "sa_sparse_decode_attn_kv4")
@@ -464,6 +461,9 @@ def _decode_kv4_checked(cache: PagedCache4, q, sel, scale, num_splits, out, lse,
     _check_selection(sel, B, Hq, dev)
     s = sel.struct()
     lib = L.load()
+    if ws is None and torch.cuda.is_current_stream_capturing():
+        # graphs may be replayed side by side: each call keeps its parts in its graph's own memory
+        ws = Workspace(dev, captured=True)
     need = lib.sa_kv4_decode_workspace_bytes(ctypes.byref(kv), Hq, num_splits)
     wp, wn, raw = _scratch(ws, dev, stream, need)
     _check(lib.sa_sparse_decode_attn_kv4(ctypes.byref(kv), q.data_ptr(), _qdtype(q), Hq, ctypes.byref(s),

@@ -16,6 +16,7 @@
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "sa.h"
@@ -202,10 +203,11 @@ PyObject *expand(PyObject *, PyObject *const *a, Py_ssize_t n)
     return Py_BuildValue("NN", THPVariable_Wrap(k), THPVariable_Wrap(v));
 }
 
-// decode(kv, page_table, seq_lens, q, idx or blocks, counts, kind, scale, num_splits, want_lse, ws, ws_bytes, stream)
+// decode(kv, page_table, seq_lens, q, idx or blocks, counts, kind, scale, num_splits, want_lse, ws, ws_bytes, stream,
+//        whether ws is the stream's default one, which captured calls do not take)
 PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    if (n != 13) return none();
+    if (n != 14) return none();
     const at::Tensor *q = tensor(a[3]), *list = tensor(a[4]), *count = tensor(a[5]);
     const int dev = device_of(q);
     sa_kv4_cache c{};
@@ -236,6 +238,15 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n)
     const size_t have = PyLong_AsSize_t(a[11]);
     if (PyErr_Occurred()) return nullptr;
     if (splits < 0 || splits > 64) return none();
+    const auto stream = static_cast<sa_stream_t>(PyLong_AsVoidPtr(a[12]));
+    if (PyObject_IsTrue(a[13])) {
+        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &capture) != cudaSuccess) {
+            cudaGetLastError();
+            return none();
+        }
+        if (capture != cudaStreamCaptureStatusNone) return none();
+    }
     const size_t need = f_decode_bytes(&c, (int32_t)H, (int32_t)splits);
     if (need == 0 || need > have) return none();
     at::Tensor out = make({B, H, D}, at::kBFloat16, dev), lse;
@@ -243,7 +254,7 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n)
     const sa_status st = f_decode(&c, ptr(q), f32 ? SA_DTYPE_F32 : SA_DTYPE_BF16, (int32_t)H, &s, (float)scale,
                                   (int32_t)splits, out.data_ptr(),
                                   lse_too ? static_cast<float *>(lse.data_ptr()) : nullptr, PyLong_AsVoidPtr(a[10]),
-                                  have, static_cast<sa_stream_t>(PyLong_AsVoidPtr(a[12])));
+                                  have, stream);
     if (PyErr_Occurred()) return nullptr;
     if (st != SA_OK) return PyLong_FromLong(st);
     if (!lse_too) Py_INCREF(Py_None);
