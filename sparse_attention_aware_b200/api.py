@@ -160,6 +160,16 @@ def _geometry(cache, device=None) -> L.KVCacheS:
                       c.max_pages_per_seq, c.num_pages)
 
 
+def _capturing() -> bool:
+    """Whether torch's current stream is being captured into a graph."""
+    return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+
+
+def _aligned(buf: torch.Tensor) -> int:
+    """Where a workspace begins in its buffer."""
+    return (buf.data_ptr() + 255) // 256 * 256
+
+
 class Workspace:
     """A reusable, zero-initialised device workspace (grows on demand).
 
@@ -168,7 +178,10 @@ class Workspace:
     call rewrites its status header and scratch.  When it grows, the old
     buffer is released with record_stream() for every stream it was handed
     to, so the caching allocator does not reuse that memory while a kernel
-    launched on one of those streams may still read it."""
+    launched on one of those streams may still read it.  A buffer that a
+    captured call was handed is kept instead: every replay of that graph writes
+    to it again, and ``status`` reads it too.  A workspace that is captured must
+    outlive its graphs."""
 
     def __init__(self, device=None, captured=False):
         self.device = device
@@ -176,12 +189,15 @@ class Workspace:
         self.buf: Optional[torch.Tensor] = None
         self._streams = []
         self._raw = {}   # stream handles in _streams -> (aligned address of buf, bytes from there on)
+        self._in_graph = False   # buf was handed to a captured call
+        self._kept = []          # outgrown buffers that were
 
     def at(self, nbytes: int, raw: int, stream=None):
         """``aligned`` for a call on the stream of handle ``raw``, without asking
         torch for its stream object when the buffer has served it before."""
         got = self._raw.get(raw)
         if got is not None and got[1] >= nbytes:
+            self._in_graph = self._in_graph or _capturing()
             return got
         ptr, n = self.aligned(nbytes + 256, stream)
         if self.buf.numel() and raw not in self._raw:
@@ -193,11 +209,15 @@ class Workspace:
             n = max(nbytes, 256)
             old = self.buf
             self.buf = self._new(n + 256, dtype=torch.uint8, device=self.device or "cuda")
-            if old is not None:
+            if old is not None and self._in_graph:
+                self._kept.append(old)
+            elif old is not None:
                 for s in self._streams:
                     old.record_stream(s)
             self._streams = []
             self._raw = {}
+            self._in_graph = False
+        self._in_graph = self._in_graph or _capturing()
         if self.buf.device.type == "cuda":
             s = stream if stream is not None else torch.cuda.current_stream(self.buf.device)
             if all(s != x for x in self._streams):
@@ -206,18 +226,18 @@ class Workspace:
 
     def aligned(self, nbytes: int, stream=None):
         buf = self.get(nbytes, stream)
-        base = buf.data_ptr()
-        off = (-base) % 256
-        return ctypes.c_void_p(base + off), buf.numel() - off
+        at = _aligned(buf)
+        return ctypes.c_void_p(at), buf.numel() - (at - buf.data_ptr())
 
     def status(self, stream=None):
         """Synchronise and return (status, detail) recorded by kernels (then cleared)."""
-        if self.buf is None:
-            return 0, (0, 0, 0)
-        ptr, _ = self.aligned(0, stream)
-        det = (L.c_i32 * 3)()
-        st = L.load().sa_read_device_status(ptr, _stream(stream), det)
-        return st, tuple(det)
+        found = 0, (0, 0, 0)
+        for buf in self._kept + ([] if self.buf is None else [self.buf]):
+            det = (L.c_i32 * 3)()
+            st = L.load().sa_read_device_status(ctypes.c_void_p(_aligned(buf)), _stream(stream), det)
+            if st != 0 and found[0] == 0:
+                found = st, tuple(det)
+        return found
 
     def raise_on_fault(self, where="device", stream=None):
         st, det = self.status(stream)
@@ -433,7 +453,7 @@ def _decode_kv4(cache: PagedCache4, q, sel, scale, num_splits, out, lse, want_ls
                 fast, wp, wn, raw = way
                 got = fast.decode(cache.kv, cache.page_table, cache.seq_lens, q, sel.idx if tok else sel.blocks,
                                   sel.count if tok else sel.block_counts, L.SEL_TOKENS if tok else L.SEL_BLOCKS, scale,
-                                  num_splits, want_lse, wp, wn, raw, ws is None)
+                                  num_splits, want_lse, wp, wn, raw)
                 if got is not None:
                     if isinstance(got, int):
                         _check(got, "sa_sparse_decode_attn_kv4")
@@ -461,7 +481,7 @@ def _decode_kv4_checked(cache: PagedCache4, q, sel, scale, num_splits, out, lse,
     _check_selection(sel, B, Hq, dev)
     s = sel.struct()
     lib = L.load()
-    if ws is None and torch.cuda.is_current_stream_capturing():
+    if ws is None and _capturing():
         # graphs may be replayed side by side: each call keeps its parts in its graph's own memory
         ws = Workspace(dev, captured=True)
     need = lib.sa_kv4_decode_workspace_bytes(ctypes.byref(kv), Hq, num_splits)

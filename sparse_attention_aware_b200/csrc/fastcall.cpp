@@ -6,7 +6,9 @@
 // are laid out as the library reads them, on the current device, with outputs
 // made here: they return the outputs, or the library's status as a number, or
 // None for any other call, which the Python code then checks, copies, places or
-// refuses as documented.  Nothing is kept between calls.
+// refuses as documented.  Calls that are being captured into a graph are left to
+// it too: it keeps the memory whose address the graph holds.  Nothing is kept
+// between calls.
 //
 // Built as _fastcall.so against torch; the library's functions are handed over
 // by address (init), so libsa is loaded in one place only.
@@ -57,6 +59,17 @@ int device_of(const at::Tensor *t)
 
 PyObject *none() { Py_RETURN_NONE; }
 
+// whether the stream (its handle as a Python number) is being captured, or cannot say
+bool captured(PyObject *stream)
+{
+    cudaStreamCaptureStatus now = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(static_cast<cudaStream_t>(PyLong_AsVoidPtr(stream)), &now) != cudaSuccess) {
+        cudaGetLastError();
+        return true;
+    }
+    return now != cudaStreamCaptureStatusNone;
+}
+
 // A 4-bit cache
 bool cache4(const at::Tensor *kv, const at::Tensor *pt, const at::Tensor *sl, int dev, sa_kv4_cache *c)
 {
@@ -74,7 +87,7 @@ bool cache4(const at::Tensor *kv, const at::Tensor *pt, const at::Tensor *sl, in
 //      free_count_out, ws, ws_bytes, stream)
 PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    if (n != 13) return none();
+    if (n != 13 || captured(a[12])) return none();
     const at::Tensor *pt = tensor(a[0]), *sl = tensor(a[1]), *add = tensor(a[2]), *fp = tensor(a[3]), *fc = tensor(a[4]);
     const at::Tensor *slo = a[8] == Py_None ? sl : tensor(a[8]), *fco = a[9] == Py_None ? fc : tensor(a[9]);
     const int dev = device_of(pt);
@@ -127,7 +140,7 @@ bool rows(const at::Tensor *x, int64_t T, int64_t H, int64_t D, int dev, int64_t
 //        interleaved, ws, ws_bytes, stream)
 PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    if (n != 17) return none();
+    if (n != 17 || captured(a[16])) return none();
     const at::Tensor *pool = tensor(a[0]), *vpool = tensor(a[1]), *pt = tensor(a[2]), *sl = tensor(a[3]);
     const at::Tensor *q = tensor(a[4]), *k = tensor(a[5]), *v = tensor(a[6]), *pos = tensor(a[7]), *slots = tensor(a[8]);
     const at::Tensor *inv = tensor(a[9]), *qw = tensor(a[10]), *kw = tensor(a[11]);
@@ -186,7 +199,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
 // expand(kv, page_table, seq_lens, pages, ws, ws_bytes, stream)
 PyObject *expand(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    if (n != 7) return none();
+    if (n != 7 || captured(a[6])) return none();
     const at::Tensor *kv = tensor(a[0]), *pages = tensor(a[3]);
     const int dev = device_of(kv);
     sa_kv4_cache c{};
@@ -203,11 +216,10 @@ PyObject *expand(PyObject *, PyObject *const *a, Py_ssize_t n)
     return Py_BuildValue("NN", THPVariable_Wrap(k), THPVariable_Wrap(v));
 }
 
-// decode(kv, page_table, seq_lens, q, idx or blocks, counts, kind, scale, num_splits, want_lse, ws, ws_bytes, stream,
-//        whether ws is the stream's default one, which captured calls do not take)
+// decode(kv, page_table, seq_lens, q, idx or blocks, counts, kind, scale, num_splits, want_lse, ws, ws_bytes, stream)
 PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    if (n != 14) return none();
+    if (n != 13 || captured(a[12])) return none();
     const at::Tensor *q = tensor(a[3]), *list = tensor(a[4]), *count = tensor(a[5]);
     const int dev = device_of(q);
     sa_kv4_cache c{};
@@ -239,14 +251,6 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (PyErr_Occurred()) return nullptr;
     if (splits < 0 || splits > 64) return none();
     const auto stream = static_cast<sa_stream_t>(PyLong_AsVoidPtr(a[12]));
-    if (PyObject_IsTrue(a[13])) {
-        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-        if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &capture) != cudaSuccess) {
-            cudaGetLastError();
-            return none();
-        }
-        if (capture != cudaStreamCaptureStatusNone) return none();
-    }
     const size_t need = f_decode_bytes(&c, (int32_t)H, (int32_t)splits);
     if (need == 0 || need > have) return none();
     at::Tensor out = make({B, H, D}, at::kBFloat16, dev), lse;
