@@ -574,8 +574,18 @@ SA_API sa_status sa_sparse_decode_attn_kv4(const sa_kv4_cache *kv, const void *q
                                            int32_t num_splits, void *out, float *lse_out, void *ws,
                                            size_t ws_bytes, sa_stream_t stream);
 
-/* Bytes of workspace the call above needs (a multiple of 256), enough for any
- * selection with num_splits 0; 0 when the description is invalid.  Host only. */
+/* The same with the splits' parts in memory of their own, and only the status
+ * word in ws (at least 256 bytes): for calls captured into graphs that are
+ * replayed side by side, whose parts must not meet while their records may.
+ *   parts  16-byte aligned, of sa_kv4_decode_workspace_bytes(...) - 256 bytes */
+SA_API sa_status sa_sparse_decode_attn_kv4_parts(const sa_kv4_cache *kv, const void *q, sa_dtype q_dtype,
+                                                 int32_t num_q_heads, const sa_selection *sel, float scale,
+                                                 int32_t num_splits, void *out, float *lse_out, void *parts,
+                                                 size_t parts_bytes, void *ws, size_t ws_bytes, sa_stream_t stream);
+
+/* Bytes of workspace sa_sparse_decode_attn_kv4 needs (a multiple of 256), enough
+ * for any selection with num_splits 0; 0 when the description is invalid.  Host
+ * only. */
 SA_API size_t sa_kv4_decode_workspace_bytes(const sa_kv4_cache *kv, int32_t num_q_heads, int32_t num_splits);
 
 /* ------------------------------------------------------------------------ */

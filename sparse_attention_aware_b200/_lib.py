@@ -25,7 +25,8 @@ EXPORTS = ("sa_select_topk", "sa_select_blocks", "sa_sparse_decode_attn", "sa_sp
            "sa_workspace_bytes", "sa_workspace_init", "sa_read_device_status", "sa_status_string",
            "sa_version", "sa_sparse_decode_attn_noalloc", "sa_fetch_pages", "sa_tier_plan",
            "sa_tier_plan_scratch_ints", "sa_check_bounded_wait", "sa_plan_append", "sa_rope_append",
-           "sa_rope_append_kv4", "sa_expand_kv4", "sa_sparse_decode_attn_kv4", "sa_kv4_decode_workspace_bytes")
+           "sa_rope_append_kv4", "sa_expand_kv4", "sa_sparse_decode_attn_kv4",
+           "sa_sparse_decode_attn_kv4_parts", "sa_kv4_decode_workspace_bytes")
 
 
 class KVCacheS(ctypes.Structure):
@@ -110,6 +111,8 @@ def load(path: str = LIB_PATH):
     L.sa_expand_kv4.argtypes = [P(KV4CacheS), c_vp, c_i32, c_vp, c_vp, c_vp, c_size, c_vp]
     L.sa_sparse_decode_attn_kv4.argtypes = [P(KV4CacheS), c_vp, c_i32, c_i32, P(SelectionS), c_f32, c_i32,
                                             c_vp, c_vp, c_vp, c_size, c_vp]
+    L.sa_sparse_decode_attn_kv4_parts.argtypes = [P(KV4CacheS), c_vp, c_i32, c_i32, P(SelectionS), c_f32, c_i32,
+                                                  c_vp, c_vp, c_vp, c_size, c_vp, c_size, c_vp]
     L.sa_kv4_decode_workspace_bytes.argtypes = [P(KV4CacheS), c_i32, c_i32]
     L.sa_kv4_decode_workspace_bytes.restype = c_size
     L.sa_check_bounded_wait.argtypes = [ctypes.c_int64, c_vp, c_size, c_vp]
@@ -125,7 +128,7 @@ def load(path: str = LIB_PATH):
     for fn in ("sa_select_topk", "sa_select_blocks", "sa_sparse_decode_attn", "sa_sparse_prefill_attn",
                "sa_workspace_init", "sa_read_device_status", "sa_sparse_decode_attn_noalloc", "sa_fetch_pages",
                "sa_tier_plan", "sa_check_bounded_wait", "sa_plan_append", "sa_rope_append", "sa_rope_append_kv4",
-               "sa_expand_kv4", "sa_sparse_decode_attn_kv4"):
+               "sa_expand_kv4", "sa_sparse_decode_attn_kv4", "sa_sparse_decode_attn_kv4_parts"):
         getattr(L, fn).restype = c_i32
     _lib = L
     return L

@@ -181,16 +181,19 @@ class Workspace:
     launched on one of those streams may still read it.  A buffer that a
     captured call was handed is kept instead: every replay of that graph writes
     to it again, and ``status`` reads it too.  A workspace that is captured must
-    outlive its graphs."""
+    outlive its graphs; one that is made by a captured call is cleared by every
+    replay of that call's graph."""
 
-    def __init__(self, device=None, captured=False):
+    def __init__(self, device=None):
         self.device = device
-        self._new = torch.empty if captured else torch.zeros   # (of one captured call: its status is not read)
         self.buf: Optional[torch.Tensor] = None
         self._streams = []
         self._raw = {}   # stream handles in _streams -> (aligned address of buf, bytes from there on)
         self._in_graph = False   # buf was handed to a captured call
         self._kept = []          # outgrown buffers that were
+
+    def _zeros(self, n: int) -> torch.Tensor:
+        return torch.zeros(n, dtype=torch.uint8, device=self.device or "cuda")
 
     def at(self, nbytes: int, raw: int, stream=None):
         """``aligned`` for a call on the stream of handle ``raw``, without asking
@@ -208,7 +211,7 @@ class Workspace:
         if self.buf is None or self.buf.numel() < nbytes:
             n = max(nbytes, 256)
             old = self.buf
-            self.buf = self._new(n + 256, dtype=torch.uint8, device=self.device or "cuda")
+            self.buf = self._zeros(n + 256)
             if old is not None and self._in_graph:
                 self._kept.append(old)
             elif old is not None:
@@ -245,6 +248,51 @@ class Workspace:
             raise SAError(st, where, det)
 
 
+def _zeros_outside_graph(n: int, device) -> torch.Tensor:
+    """Zeroed device memory that belongs to no graph, while torch's current stream
+    is being captured: made, cleared and waited for on a stream that is not.
+    (Memory of a graph's pool would be cleared by its replays, and not before
+    the first.)"""
+    lib = ctypes.CDLL("libcuda.so.1")
+    mode = ctypes.c_int(2)   # relaxed: other streams may be waited for
+    lib.cuThreadExchangeStreamCaptureMode(ctypes.byref(mode))
+    try:
+        while True:   # (torch hands its streams out in turn, the captured one too)
+            side = torch.cuda.Stream(device)
+            with torch.cuda.stream(side):
+                if not torch.cuda.is_current_stream_capturing():
+                    buf = torch.zeros(n, dtype=torch.uint8, device=device)
+                    break
+        side.synchronize()
+    finally:
+        lib.cuThreadExchangeStreamCaptureMode(ctypes.byref(mode))
+    return buf
+
+
+class _DefaultWorkspace(Workspace):
+    """The workspace of a stream's calls that were given none.  It lives as long as
+    the process, and so it may be made by a captured call."""
+
+    def _zeros(self, n: int) -> torch.Tensor:
+        return _zeros_outside_graph(n, self.device) if _capturing() else super()._zeros(n)
+
+
+def device_status(device=None):
+    """(status, detail) of the calls on ``device`` (the current one) that were
+    given no workspace: the first record found in their streams' workspaces, which
+    are then cleared.  Waits for the device.  Replays of such calls that were
+    captured record here too."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    found = 0, (0, 0, 0)
+    with torch.cuda.device(dev):
+        torch.cuda.synchronize()
+        for ws in list(_default_ws.values()):
+            if ws.buf is not None and ws.buf.device.type == "cuda" and ws.buf.device.index == torch.cuda.current_device():
+                got = ws.status()
+                found = got if found[0] == 0 else found
+    return found
+
+
 _default_ws = {}
 _default_ws_at = {}   # (device index, stream handle) -> the same workspaces
 
@@ -275,7 +323,7 @@ def _ws(ws: Optional[Workspace], device, stream=None) -> Workspace:
         sid = 0
     key = (str(dev), sid)
     if key not in _default_ws:
-        _default_ws[key] = Workspace(device)
+        _default_ws[key] = _DefaultWorkspace(device)
     return _default_ws[key]
 
 
@@ -418,7 +466,8 @@ def sparse_decode_attn(cache, q: torch.Tensor, sel, scale: Optional[float] = Non
     list, 1 by default; over a PagedCache4 0, the default there, lets the
     library choose.  Captured into a graph without ``ws``, a call over a
     PagedCache4 keeps its parts in that graph's memory, so that graphs may be
-    replayed side by side.  Returns (out bf16, lse fp32)."""
+    replayed side by side; what its replays record, ``device_status`` reads.
+    Returns (out bf16, lse fp32)."""
     if isinstance(cache, PagedCache4):
         return _decode_kv4(cache, q, sel, scale, 0 if num_splits is None else num_splits, out, lse, want_lse, ws, stream)
     if num_splits is None:
@@ -481,15 +530,19 @@ def _decode_kv4_checked(cache: PagedCache4, q, sel, scale, num_splits, out, lse,
     _check_selection(sel, B, Hq, dev)
     s = sel.struct()
     lib = L.load()
+    need = lib.sa_kv4_decode_workspace_bytes(ctypes.byref(kv), Hq, num_splits)
+    call = (ctypes.byref(kv), q.data_ptr(), _qdtype(q), Hq, ctypes.byref(s),
+            1.0 / math.sqrt(d) if scale is None else scale, num_splits, out.data_ptr(),
+            None if lse is None else lse.data_ptr())
     if ws is None and _capturing():
         # graphs may be replayed side by side: each call keeps its parts in its graph's own memory
-        ws = Workspace(dev, captured=True)
-    need = lib.sa_kv4_decode_workspace_bytes(ctypes.byref(kv), Hq, num_splits)
+        wp, wn, raw = _scratch(None, dev, stream, 256)
+        parts = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        _check(lib.sa_sparse_decode_attn_kv4_parts(*call, parts.data_ptr(), parts.numel(), wp, wn, raw),
+               "sa_sparse_decode_attn_kv4_parts")
+        return out, lse
     wp, wn, raw = _scratch(ws, dev, stream, need)
-    _check(lib.sa_sparse_decode_attn_kv4(ctypes.byref(kv), q.data_ptr(), _qdtype(q), Hq, ctypes.byref(s),
-                                         1.0 / math.sqrt(d) if scale is None else scale, num_splits, out.data_ptr(),
-                                         None if lse is None else lse.data_ptr(), wp, wn, raw),
-           "sa_sparse_decode_attn_kv4")
+    _check(lib.sa_sparse_decode_attn_kv4(*call, wp, wn, raw), "sa_sparse_decode_attn_kv4")
     return out, lse
 
 

@@ -612,9 +612,10 @@ size_t sa_kv4_decode_workspace_bytes(const sa_kv4_cache *kv, int32_t num_q_heads
     return sa::decode_workspace_bytes(&as, num_q_heads, most);
 }
 
-sa_status sa_sparse_decode_attn_kv4(const sa_kv4_cache *kv, const void *q, sa_dtype q_dtype, int32_t num_q_heads,
-                                    const sa_selection *sel, float scale, int32_t num_splits, void *out,
-                                    float *lse_out, void *ws, size_t ws_bytes, sa_stream_t stream)
+sa_status sa_sparse_decode_attn_kv4_parts(const sa_kv4_cache *kv, const void *q, sa_dtype q_dtype,
+                                          int32_t num_q_heads, const sa_selection *sel, float scale,
+                                          int32_t num_splits, void *out, float *lse_out, void *parts,
+                                          size_t parts_bytes, void *ws, size_t ws_bytes, sa_stream_t stream)
 {
     DecodeArgs a{};
     sa_status st = check_cache4(kv, &a.c);
@@ -623,8 +624,10 @@ sa_status sa_sparse_decode_attn_kv4(const sa_kv4_cache *kv, const void *q, sa_dt
     st = check_decode(kv->batch, kv->num_kv_heads, q, q_dtype, num_q_heads, sel, scale, out, lse_out, &a);
     if (st != SA_OK) return st;
     if (kv->batch > 65535 || num_q_heads > 65535) return SA_ERR_UNSUPPORTED;   // grid dimensions
-    st = check_ws(ws, ws_bytes, sa_kv4_decode_workspace_bytes(kv, num_q_heads, num_splits));
+    st = check_ws(ws, ws_bytes, kHeader);
     if (st != SA_OK) return st;
+    if (!parts || !aligned(parts, 16) || parts_bytes < sa_kv4_decode_workspace_bytes(kv, num_q_heads, num_splits) - kHeader)
+        return SA_ERR_WORKSPACE;
     if (num_splits == 0) {
         const bool wide = a.blocks && num_q_heads / kv->num_kv_heads > 8;
         num_splits = decode_kv4_splits(kv->batch, a.blocks ? kv4_group_rows(kv, num_q_heads) : num_q_heads,
@@ -633,15 +636,24 @@ sa_status sa_sparse_decode_attn_kv4(const sa_kv4_cache *kv, const void *q, sa_dt
         const int most = kv4_most_splits(kv, num_q_heads);
         if (num_splits > most) num_splits = most;
     }
-    char *w = static_cast<char *>(ws);
+    char *w = static_cast<char *>(parts);
     const size_t rows = (size_t)kv->batch * num_q_heads;
     a.S = num_splits;
-    a.part_o = reinterpret_cast<float *>(w + kHeader);
-    a.part_ml = reinterpret_cast<float *>(w + kHeader + up(rows * num_splits * kv->head_dim * sizeof(float)));
+    a.part_o = reinterpret_cast<float *>(w);
+    a.part_ml = reinterpret_cast<float *>(w + up(rows * num_splits * kv->head_dim * sizeof(float)));
     a.out = static_cast<uint16_t *>(out);
     a.lse = lse_out;
     a.st = static_cast<DevStatus *>(ws);
     return cuda_status(launch_decode_kv4(a, (cudaStream_t)stream));
+}
+
+sa_status sa_sparse_decode_attn_kv4(const sa_kv4_cache *kv, const void *q, sa_dtype q_dtype, int32_t num_q_heads,
+                                    const sa_selection *sel, float scale, int32_t num_splits, void *out,
+                                    float *lse_out, void *ws, size_t ws_bytes, sa_stream_t stream)
+{
+    void *parts = ws && ws_bytes >= kHeader ? static_cast<char *>(ws) + kHeader : nullptr;
+    return sa_sparse_decode_attn_kv4_parts(kv, q, q_dtype, num_q_heads, sel, scale, num_splits, out, lse_out, parts,
+                                           parts ? ws_bytes - kHeader : 0, ws, ws_bytes, stream);
 }
 
 }  // extern "C"
