@@ -428,7 +428,9 @@ SA_API int64_t sa_tier_plan_scratch_ints(int64_t host_pages, int32_t slots);
  * are free, more free pages than num_free: SA_ERR_CAPACITY) is recorded and
  * changes nothing: lengths and free count are copied, cu_tokens is 0 and every
  * slot -1.  A page number out of [0, num_pages) in the table or on the stack is
- * recorded; its tokens get slot -1 (and a fresh table entry -1).
+ * recorded; its tokens get slot -1 (and a fresh table entry -1).  That of an ended
+ * sequence stays off the stack; a step that lacks pages without it changes
+ * nothing, as above.  (Entries of the stack past the free count may change.)
  *   page_size in {16, 64}, batch <= 4096 (SA_ERR_UNSUPPORTED otherwise).
  *   ws  any workspace of at least 256 bytes (only its status word is used).
  */

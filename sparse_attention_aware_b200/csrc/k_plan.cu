@@ -8,7 +8,8 @@
 //   held_b = ceil(n_b / P),  need_b = ceil((n_b + a_b) / P) - held_b
 // The pages of ended sequences go onto a stack of free pages in (sequence,
 // page) order, then the i-th page needed, counted in the same order, is the
-// i-th from the top.  Token i of the step belongs to the sequence b with
+// i-th from the top.  (A number that names no page is no page of the sequence:
+// it stays off the stack, and the pages above it move down.)  Token i of the step belongs to the sequence b with
 // cu_b <= i < cu_{b+1} (cu: prefix sums of a), has position n_b + i - cu_b and
 // goes to slot page * P + position % P.
 //
@@ -18,7 +19,9 @@
 // free count can be updated in place -- and then share the writing of tables
 // and tokens.  Bound by latency: the dependent trips lengths -> scan -> stack
 // -> table, about 16 bytes per token beside them.  Measured: 32 sequences of one
-// token 4.7 us (one CTA), 256 sequences with up to 131072 tokens 9.8 us.
+// token 4.4 us (one CTA), 256 sequences with up to 131072 tokens 10.3 us (0.5 us of
+// it for the barrier behind which CTAs may tell each other of a number that is no
+// page).
 #include <cooperative_groups.h>
 
 #include "sa_internal.h"
@@ -69,6 +72,8 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums *warp_sum, Sums &total)
     return r;
 }
 
+// ONE: the cluster is this CTA alone, and its barrier the CTA's
+template <bool ONE>
 __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
 {
     pdl_wait();
@@ -76,13 +81,24 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
     namespace cg = cooperative_groups;
     extern __shared__ int plan_sm[];
     __shared__ Sums warp_sum[32];
+    __shared__ int s_none, s_kept;   // whether a CTA was to push what is no page; how many pages the stack got
     const int B = a.B, P = 1 << a.Plog2, tid = threadIdx.x;
     int *s_old = plan_sm;            // [B] tokens held
     int *s_new = s_old + B;          // [B] tokens to come, -1 = ended
     int *s_need = s_new + B;         // [B] fresh pages of earlier sequences (of an ended one: freed pages)
     int *s_cu = s_need + B;          // [B + 1]
-    const int rank = (int)cg::this_cluster().block_rank(), ranks = (int)cg::this_cluster().num_blocks();
+    const int rank = ONE ? 0 : (int)cg::this_cluster().block_rank(), ranks = ONE ? 1 : (int)cg::this_cluster().num_blocks();
+    auto meet = [] {
+        if (ONE) __syncthreads();
+        else cg::this_cluster().sync();
+    };
+    auto tell = [&](int *mine, int value) {   // every CTA's copy of a shared variable, by one warp
+        if (ONE) *mine = value;
+        else if ((tid & 31) < ranks) *cg::this_cluster().map_shared_rank(mine, tid & 31) = value;
+    };
     const long long Lcap = (long long)a.max_pages << a.Plog2;
+    if (tid == 0) s_none = 0;
+    if (!ONE) asm volatile("barrier.cluster.arrive;" ::: "memory");   // s_none may be written by the others
 
     // ---- lengths, and what they ask for
     Sums mine = {0, 0, 0};
@@ -127,7 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
     }
     // a step that cannot be taken changes nothing
     if (bad) all = {0, 0, 0};
-    const int top = count + (int)all.back;
+    int top = count + (int)all.back;
 #pragma unroll
     for (int u = 0; u < kPlanItems; ++u) {
         const int b = tid * kPlanItems + u;
@@ -139,6 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
     if (tid == 0) s_cu[B] = (int)all.tok;
     __syncthreads();
     const int gtid = rank * kPlanThreads + tid, threads = ranks * kPlanThreads, lane = tid & 31;
+    bool none = false;   // one that is no page
     if (!bad && all.back > 0) {
         // pages of ended sequences onto the stack, a warp a sequence
         for (int b = gtid >> 5; b < B; b += threads >> 5) {
@@ -152,13 +169,40 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
 #pragma unroll
                 for (int u = 0; u < kRows; ++u) {
                     if (p + 32 * u >= held) break;
-                    if (page[u] < 0 || page[u] >= a.num_pages) fault(a.st, CHK_PAGE, page[u]);
+                    if (page[u] < 0 || page[u] >= a.num_pages) {
+                        fault(a.st, CHK_PAGE, page[u]);
+                        none = true;
+                    }
                     a.free[count + s_need[b] + p + 32 * u] = page[u];
                 }
             }
         }
     }
-    cg::this_cluster().sync();   // every CTA has read the inputs; the stack is whole
+    if (!ONE) asm volatile("barrier.cluster.wait;" ::: "memory");
+    if (__any_sync(~0u, none)) tell(&s_none, 1);
+    meet();   // every CTA has read the inputs; the stack is whole
+    if (__builtin_expect(s_none != 0, 0)) {   // (set in all CTAs or in none)
+        if (gtid < 32) {
+            int kept = 0;
+            for (int i = lane; i - lane < (int)all.back; i += 32) {
+                const int page = i < (int)all.back ? a.free[count + i] : -1;
+                const bool fine = page >= 0 && page < a.num_pages;
+                const unsigned m = __ballot_sync(~0u, fine);   // (and every lane has read its number)
+                if (fine) a.free[count + kept + __popc(m & ((1u << lane) - 1))] = page;
+                kept += __popc(m);
+                __syncwarp();
+            }
+            tell(&s_kept, kept);
+        }
+        meet();
+        top = count + s_kept;
+        if (all.need > top) {   // not enough without them (and recorded already)
+            bad = 1;
+            all = {0, 0, 0};
+            for (int b = tid; b <= B; b += kPlanThreads) s_cu[b] = 0;
+            __syncthreads();
+        }
+    }
 
     // ---- lengths, prefix sums, fresh table entries
     for (int b = gtid; b < B; b += threads) {
@@ -242,17 +286,19 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
 
 cudaError_t launch_plan(const PlanArgs &a, cudaStream_t s)
 {
+    // a step's few tokens need one CTA (4.4 us for 32); 131072 take 11.7 us with
+    // 16 CTAs and 14.8 with 8
+    const int ctas = a.max_tokens > 32 * kPlanThreads ? 16 : a.max_tokens > 4 * kPlanThreads || a.B > kPlanThreads ? 8 : 1;
+    auto kern = ctas == 1 ? k_plan_append<true> : k_plan_append<false>;
     const size_t smem = (size_t)(4 * a.B + 1) * sizeof(int);
     if (smem > 40960) {   // (static shared memory comes on top, up to 48 KB together without asking)
-        cudaError_t e = cudaFuncSetAttribute(k_plan_append, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (4 * kPlanMaxBatch + 1) * (int)sizeof(int));
         if (e != cudaSuccess) return e;
     }
-    // a step's few tokens need one CTA (4.7 us for 32); 131072 take 11.7 us with
-    // 16 CTAs and 14.8 with 8
-    const int ctas = a.max_tokens > 32 * kPlanThreads ? 16 : a.max_tokens > 4 * kPlanThreads || a.B > kPlanThreads ? 8 : 1;
+    if (ctas == 1) return launch_pdl(kern, dim3(1), dim3(kPlanThreads), smem, s, a);
     if (ctas > 8) {
-        cudaError_t e = cudaFuncSetAttribute(k_plan_append, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -268,7 +314,7 @@ cudaError_t launch_plan(const PlanArgs &a, cudaStream_t s)
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_plan_append, a);
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace sa
