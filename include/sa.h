@@ -568,7 +568,10 @@ SA_API sa_status sa_expand_kv4(const sa_kv4_cache *kv, const int32_t *pages, int
  * fp32 query enters as two fp16 parts, 22 bits); a softmax weight times its
  * row's scale enters the P.V product as fp16, scaled by a power of two.  A selected row that was stored as NaN makes
  * the outputs of its heads NaN.
- *   num_splits in [0, 64]; 0 lets the library choose from the sizes.
+ *   num_splits in [0, 64]; 0 lets the library choose from the sizes: k_cap, or
+ *     max_blocks pages, is taken for what the longest list holds, so that a capacity
+ *     far above that is better given with a count (or made smaller).  The order of
+ *     the sums, and so the last bits, go by the count.
  *   ws  workspace of sa_kv4_decode_workspace_bytes(...) bytes
  */
 SA_API sa_status sa_sparse_decode_attn_kv4(const sa_kv4_cache *kv, const void *q, sa_dtype q_dtype,

@@ -464,7 +464,8 @@ def sparse_decode_attn(cache, q: torch.Tensor, sel, scale: Optional[float] = Non
     """Split-KV sparse decode + combine (``sa_sparse_decode_attn``, or
     ``sa_sparse_decode_attn_kv4`` over a PagedCache4).  ``num_splits`` parts a
     list, 1 by default; over a PagedCache4 0, the default there, lets the
-    library choose.  Captured into a graph without ``ws``, a call over a
+    library choose by the selection's capacity (for masks far below the context
+    give ``select_blocks_spans`` the ``max_blocks`` they need).  Captured into a graph without ``ws``, a call over a
     PagedCache4 keeps its parts in that graph's memory, so that graphs may be
     replayed side by side; what its replays record, ``device_status`` reads.
     Returns (out bf16, lse fp32)."""

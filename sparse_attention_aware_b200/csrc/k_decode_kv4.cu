@@ -878,23 +878,37 @@ cudaError_t launch_kind(const DecodeArgs &a, cudaStream_t s)
 // `start` beside `each` a token when its SM is full, less when it is not; CTAs
 // that all run at once take as long as one of the longest row, more of them fill
 // the slots with falling sizes (split_at), the first of which must fit in as well,
-// and leave a tail.  The sequences of a batch differ, so their block lists are taken
-// to hold 0.72 of the longest one's entries on average (lengths spread over a factor
-// of 2).  The constants are fitted to measured times (us, head_dim 128):
-//   32 x 8 groups of up to 16384 tokens  3, 4, 5, 6, 8 splits   87, 81, 80, 80, 83
-//   16 x 8 (8 heads each)                3, 4, 6, 8, 10, 16     64, 69, 54, 51, 52, 57
-//   64 x 8 groups of up to 4096          1, 2, 3, 4             57, 50, 53, 56
-//   1 x 8 groups of 131072 tokens        24, 37, 55, 64         41, 37, 37, 42
-//   4 x 8 groups of a masked step        4, 8, 13               11.5, 9.9, 11.4
-//   32 x 32 lists of 4096 tokens         1, 2, 3, 4             150, 141, 144, 151
-//   8 x 32 lists of 2048 tokens          1, 2, 3, 4             34, 27, 26, 27
+// and leave a tail.  The rule sees the lists' capacity alone, not what they hold:
+// a capacity far above that costs splits (a masked step of 4 sequences with 8 groups:
+// 10.2 us with the 256 entries it needs, 13.3 with the 8194 of its whole context).
+//
+// `filled`, what a batch's block lists hold of it on average, stands between
+// sequences of one length and ragged ones, because a count chosen for the one must not
+// be bad for the other.  Measured over batches of equal lengths, of lengths spread
+// over a factor of 2 and of lengths spread evenly from 2% up: with 1.0 the chosen
+// counts are up to 23%, 47% and 73% slower than the best of each batch, with 0.76
+// 7%, 5% and 18%.  Times (us, head_dim 128) of equal | ragged | evenly spread
+// lengths, * the chosen count:
+//   32 x 8 groups (4 heads) of 16384     4*, 6, 8         107 107 113 | 85 84 87 | 68 64 66
+//   16 x 8 groups (8 heads) of 16384     3, 5, 8*, 10     69 66 64 65 | 66 62 54 56 | 58 52 41 40
+//   16 x 2 groups (8) of 65536           13, 24, 32*      66 70 67 | 63 57 56 | 55 49 43
+//   32 x 4 groups (8) of 16384           3, 5, 8*, 10     69 66 64 65 | 66 61 52 54 | 63 56 42 43
+//    8 x 4 groups (12) of 65536          10, 16, 20, 22*  136 97 101 104 | 135 90 81 82 | 129 88 74 70
+//  128 x 8 groups (4) of 4096            1*, 2, 3         104 111 123 | 93 91 97 | 70 68 75
+//   64 x 8 groups (4) of 4096            1, 2*, 3         65 59 63 | 59 51 52 | 43 39 41
+//    4 x 8 groups (8) of 32768           8, 13*, 24, 32   40 38 42 41 | 40 37 36 37 | 40 36 32 31
+// and of lists of one sequence, and token lists:
+//    1 x 8 groups of 131072 tokens       24, 37, 55, 64   41, 37, 37, 42
+//    4 x 8 groups of a masked step       4, 8*, 13        11.9, 10.2, 12.2
+//   32 x 32 lists of 4096 tokens         1, 2*, 3, 4      150, 141, 144, 151
+//    8 x 32 lists of 2048 tokens         1, 2*, 3, 4      34, 27, 26, 27
 int decode_kv4_splits(int B, int rows, long long list, int D, bool tokens, bool f32, bool wide)
 {
     const double units = (double)B * rows, start = 4.0;
     if (units <= 0 || list <= 0) return 1;
     const double slots = 148.0 * (wide ? 2 : tokens && !f32 ? 4 : 3);
     const double each = (tokens ? 0.0176 : wide ? 0.013 : 0.0095) * (D + 32) / 160;
-    const double filled = tokens || B == 1 ? 1.0 : 0.72;
+    const double filled = tokens || B == 1 ? 1.0 : 0.76;
     int best = 1;
     double least = 0;
     for (int S = 1; S <= 64; ++S) {
@@ -906,7 +920,7 @@ int decode_kv4_splits(int B, int rows, long long list, int D, bool tokens, bool 
         } else {
             const double first = start + each * list * (2.0 * S - 1) / ((double)S * S);
             t = (ctas * start + filled * units * list * each) / slots;
-            t = (t > first ? t : first) + start + each * n / (2 * S);
+            t = (t > first ? t : first) + start + each * n / (4 * S);
         }
         if (S > 1) t += 1.2 + (S + 7) / 8;   // the combine: a trip to memory for 8 splits
         if (S == 1 || t < least) {
