@@ -12,6 +12,7 @@ import dataclasses
 import functools
 import inspect
 import math
+import warnings
 from typing import Optional, Sequence
 
 import torch
@@ -46,10 +47,16 @@ def _stream(stream=None):
 
 def _load_fast():
     """The native short way of the calls below (csrc/fastcall.cpp), set up with
-    libsa's entry points; None where it has not been built."""
+    libsa's entry points; None, with a warning, where it has not been built for
+    this torch and Python (it uses torch's own C++ classes)."""
+    from . import build
     try:
+        if not build.fastcall_fits():
+            raise ImportError("%s is missing, or compiled against another torch or Python" % build.FAST)
         from . import _fastcall
-    except ImportError:
+    except ImportError as e:
+        warnings.warn("calls take 8 to 20 us longer without the binding's native calls (%s); "
+                      "python -m sparse_attention_aware_b200.build makes them" % e, RuntimeWarning)
         return None
     lib = L.load()
     _fastcall.init(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in

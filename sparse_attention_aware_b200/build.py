@@ -41,11 +41,26 @@ def nvcc() -> str:
     return "nvcc"
 
 
+def _made_for() -> str:
+    """What the native calls are compiled against, as they carry it."""
+    import torch
+    return "sa-fastcall for torch %s, python %d.%d;" % (torch.__version__, *sys.version_info[:2])
+
+
+def fastcall_fits() -> bool:
+    """Whether there are native calls, and compiled against this torch and Python."""
+    try:
+        with open(FAST, "rb") as f:
+            return _made_for().encode() in f.read()
+    except OSError:
+        return False
+
+
 def build_fastcall(force: bool = False) -> str:
     """The short calls of the binding, a Python module against torch's own
     libraries (already loaded by whoever imports it)."""
     deps = [FAST_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(FAST) and all(os.path.getmtime(p) <= os.path.getmtime(FAST) for p in deps):
+    if not force and fastcall_fits() and all(os.path.getmtime(p) <= os.path.getmtime(FAST) for p in deps):
         return FAST
     import torch
     base = os.path.dirname(torch.__file__)
@@ -53,7 +68,7 @@ def build_fastcall(force: bool = False) -> str:
     cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.sep in nvcc() else "/usr/local/cuda"
     subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
                     "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
-                    "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
+                    '-DSA_MADE_FOR="%s"' % _made_for(), "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
                     "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
                     "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
                     FAST_SRC, "-o", tmp, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cuda",

@@ -43,3 +43,35 @@ def test_a_library_that_does_not_build_is_an_error(monkeypatch, place):
     monkeypatch.setattr(subprocess, "run", run)
     with pytest.raises(subprocess.CalledProcessError):
         B.build(force=True)
+
+
+def test_native_calls_compiled_against_another_torch_are_built_again(monkeypatch, place):
+    import torch
+    ran, at = place
+    made = B._made_for()
+    monkeypatch.setattr(subprocess, "run", lambda cmd, check: (
+        ran.append(cmd), open(cmd[cmd.index("-o") + 1], "wb").write(made.encode())))
+    B.build_fastcall()
+    assert len(ran) == 1 and B.fastcall_fits()
+    B.build_fastcall()
+    assert len(ran) == 1                                  # up to date
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert not B.fastcall_fits()
+    made = B._made_for()
+    B.build_fastcall()
+    assert len(ran) == 2 and "0.0.1" in " ".join(ran[-1]) and B.fastcall_fits()
+
+
+@pytest.mark.parametrize("content", [None, b"of another torch"])
+def test_native_calls_that_do_not_fit_are_not_loaded(monkeypatch, tmp_path, content):
+    from sparse_attention_aware_b200 import api
+    monkeypatch.setattr(B, "FAST", str(tmp_path / "_fastcall.so"))
+    if content is not None:
+        (tmp_path / "_fastcall.so").write_bytes(content)
+    with pytest.warns(RuntimeWarning, match="native calls"):
+        assert api._load_fast() is None
+
+
+def test_the_built_native_calls_fit():
+    B.build()
+    assert B.fastcall_fits()
