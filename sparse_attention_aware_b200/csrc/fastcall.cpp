@@ -59,6 +59,13 @@ int device_of(const at::Tensor *t)
 
 PyObject *none() { Py_RETURN_NONE; }
 
+// Python's other threads run while one lives: an allocation or a launch may wait,
+// for instance for room in the stream's queue
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // whether the stream (its handle as a Python number) is being captured, or cannot say
 bool captured(PyObject *stream)
 {
@@ -97,8 +104,7 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n)
         !is(fp, at::kInt, fp->sizes(), dev) || !is(fc, at::kInt, {1}, dev) || !is(slo, at::kInt, {B}, dev) ||
         !is(fco, at::kInt, {1}, dev) || tokens < 0 || tokens > INT32_MAX)
         return none();
-    at::Tensor cu = make({B + 1}, at::kInt, dev), pos = make({tokens}, at::kInt, dev),
-               slots = make({tokens}, at::kLong, dev), seq = make({tokens}, at::kInt, dev);
+    at::Tensor cu, pos, slots, seq;
     sa_plan_args p{};
     p.page_table = static_cast<int32_t *>(ptr(pt));
     p.seq_lens = static_cast<int32_t *>(ptr(sl));
@@ -107,19 +113,27 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n)
     p.free_count = static_cast<int32_t *>(ptr(fc));
     p.seq_lens_out = static_cast<int32_t *>(ptr(slo));
     p.free_count_out = static_cast<int32_t *>(ptr(fco));
-    p.cu_tokens = static_cast<int32_t *>(cu.data_ptr());
-    p.positions = static_cast<int32_t *>(pos.data_ptr());
-    p.slots = static_cast<int64_t *>(slots.data_ptr());
-    p.seq_ids = static_cast<int32_t *>(seq.data_ptr());
     p.batch = (int32_t)B;
     p.page_size = (int32_t)PyLong_AsLong(a[6]);
     p.max_pages_per_seq = (int32_t)pt->size(1);
     p.num_pages = (int32_t)PyLong_AsLong(a[5]);
     p.num_free = (int32_t)fp->numel();
     p.max_tokens = (int32_t)tokens;
-    const sa_status st = f_plan(&p, PyLong_AsVoidPtr(a[10]), PyLong_AsSize_t(a[11]),
-                                static_cast<sa_stream_t>(PyLong_AsVoidPtr(a[12])));
+    void *ws = PyLong_AsVoidPtr(a[10]);
+    const size_t wn = PyLong_AsSize_t(a[11]);
+    const auto stream = static_cast<sa_stream_t>(PyLong_AsVoidPtr(a[12]));
     if (PyErr_Occurred()) return nullptr;
+    sa_status st;
+    {
+        Unlocked threads;
+        cu = make({B + 1}, at::kInt, dev), pos = make({tokens}, at::kInt, dev);
+        slots = make({tokens}, at::kLong, dev), seq = make({tokens}, at::kInt, dev);
+        p.cu_tokens = static_cast<int32_t *>(cu.data_ptr());
+        p.positions = static_cast<int32_t *>(pos.data_ptr());
+        p.slots = static_cast<int64_t *>(slots.data_ptr());
+        p.seq_ids = static_cast<int32_t *>(seq.data_ptr());
+        st = f_plan(&p, ws, wn, stream);
+    }
     if (st != SA_OK) return PyLong_FromLong(st);
     return Py_BuildValue("NNNN", THPVariable_Wrap(cu), THPVariable_Wrap(pos), THPVariable_Wrap(slots),
                          THPVariable_Wrap(seq));
@@ -171,11 +185,10 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (wt != at::kBFloat16 && wt != at::kFloat) return none();
     if (qw ? !is(qw, wt, {D}, dev) : a[10] != Py_None) return none();
     if (kw ? !is(kw, wt, {D}, dev) : a[11] != Py_None) return none();
-    at::Tensor out = make({T, Hq, D}, at::kBFloat16, dev);
+    at::Tensor out;
     p.q = ptr(q);
     p.k = ptr(k);
     p.v = ptr(v);
-    p.q_out = out.data_ptr();
     p.q_out_stride = Hq * D;
     p.positions = static_cast<const int32_t *>(ptr(pos));
     p.slots = static_cast<const int64_t *>(ptr(slots));
@@ -192,7 +205,13 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
     const size_t wn = PyLong_AsSize_t(a[15]);
     sa_stream_t st = static_cast<sa_stream_t>(PyLong_AsVoidPtr(a[16]));
     if (PyErr_Occurred()) return nullptr;
-    const sa_status r = four ? f_append4(&c4, &p, ws, wn, st) : f_append(&c16, &p, ws, wn, st);
+    sa_status r;
+    {
+        Unlocked threads;
+        out = make({T, Hq, D}, at::kBFloat16, dev);
+        p.q_out = out.data_ptr();
+        r = four ? f_append4(&c4, &p, ws, wn, st) : f_append(&c16, &p, ws, wn, st);
+    }
     return r == SA_OK ? THPVariable_Wrap(out) : PyLong_FromLong(r);
 }
 
@@ -206,12 +225,19 @@ PyObject *expand(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (dev < 0 || !cache4(kv, tensor(a[1]), tensor(a[2]), dev, &c)) return none();
     if (!pages || !is(pages, at::kInt, {pages->numel()}, dev)) return none();
     const int64_t m = pages->numel();
-    at::Tensor k = make({m, c.num_kv_heads, c.page_size, c.head_dim}, at::kBFloat16, dev);
-    at::Tensor v = make({m, c.num_kv_heads, c.page_size, c.head_dim}, at::kBFloat16, dev);
-    const sa_status st = f_expand(&c, static_cast<const int32_t *>(ptr(pages)), (int32_t)m, k.data_ptr(), v.data_ptr(),
-                                  PyLong_AsVoidPtr(a[4]), PyLong_AsSize_t(a[5]),
-                                  static_cast<sa_stream_t>(PyLong_AsVoidPtr(a[6])));
+    const int32_t *list = static_cast<const int32_t *>(ptr(pages));
+    void *ws = PyLong_AsVoidPtr(a[4]);
+    const size_t wn = PyLong_AsSize_t(a[5]);
+    const auto stream = static_cast<sa_stream_t>(PyLong_AsVoidPtr(a[6]));
     if (PyErr_Occurred()) return nullptr;
+    at::Tensor k, v;
+    sa_status st;
+    {
+        Unlocked threads;
+        k = make({m, c.num_kv_heads, c.page_size, c.head_dim}, at::kBFloat16, dev);
+        v = make({m, c.num_kv_heads, c.page_size, c.head_dim}, at::kBFloat16, dev);
+        st = f_expand(&c, list, (int32_t)m, k.data_ptr(), v.data_ptr(), ws, wn, stream);
+    }
     if (st != SA_OK) return PyLong_FromLong(st);
     return Py_BuildValue("NN", THPVariable_Wrap(k), THPVariable_Wrap(v));
 }
@@ -247,19 +273,23 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n)
     const double scale = a[7] == Py_None ? 1.0 / std::sqrt((double)D) : PyFloat_AsDouble(a[7]);
     const long splits = PyLong_AsLong(a[8]);
     const int lse_too = PyObject_IsTrue(a[9]);
+    void *ws = PyLong_AsVoidPtr(a[10]);
     const size_t have = PyLong_AsSize_t(a[11]);
+    const auto stream = static_cast<sa_stream_t>(PyLong_AsVoidPtr(a[12]));
     if (PyErr_Occurred()) return nullptr;
     if (splits < 0 || splits > 64) return none();
-    const auto stream = static_cast<sa_stream_t>(PyLong_AsVoidPtr(a[12]));
     const size_t need = f_decode_bytes(&c, (int32_t)H, (int32_t)splits);
     if (need == 0 || need > have) return none();
-    at::Tensor out = make({B, H, D}, at::kBFloat16, dev), lse;
-    if (lse_too) lse = make({B, H}, at::kFloat, dev);
-    const sa_status st = f_decode(&c, ptr(q), f32 ? SA_DTYPE_F32 : SA_DTYPE_BF16, (int32_t)H, &s, (float)scale,
-                                  (int32_t)splits, out.data_ptr(),
-                                  lse_too ? static_cast<float *>(lse.data_ptr()) : nullptr, PyLong_AsVoidPtr(a[10]),
-                                  have, stream);
-    if (PyErr_Occurred()) return nullptr;
+    const void *queries = ptr(q);
+    at::Tensor out, lse;
+    sa_status st;
+    {
+        Unlocked threads;
+        out = make({B, H, D}, at::kBFloat16, dev);
+        if (lse_too) lse = make({B, H}, at::kFloat, dev);
+        st = f_decode(&c, queries, f32 ? SA_DTYPE_F32 : SA_DTYPE_BF16, (int32_t)H, &s, (float)scale, (int32_t)splits,
+                      out.data_ptr(), lse_too ? static_cast<float *>(lse.data_ptr()) : nullptr, ws, have, stream);
+    }
     if (st != SA_OK) return PyLong_FromLong(st);
     if (!lse_too) Py_INCREF(Py_None);
     return Py_BuildValue("NN", THPVariable_Wrap(out), lse_too ? THPVariable_Wrap(lse) : Py_None);
