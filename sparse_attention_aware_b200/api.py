@@ -12,6 +12,7 @@ import dataclasses
 import functools
 import inspect
 import math
+import operator
 import warnings
 from typing import Optional, Sequence
 
@@ -353,6 +354,12 @@ def _need(t: torch.Tensor, shape, dtype, device, what: str) -> None:
                          % (what, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
 
 
+def _int32(x, what: str) -> None:
+    """A size that the library takes as 32 bits (ctypes would cut it)."""
+    if not -2 ** 31 <= operator.index(x) < 2 ** 31:
+        raise ValueError("%s: %d needs more than 32 bits" % (what, x))
+
+
 def _bf16_q(q: torch.Tensor, what: str) -> torch.Tensor:
     if q.dtype != torch.bfloat16:
         raise TypeError("%s: q must be bf16, got %s" % (what, q.dtype))
@@ -522,6 +529,7 @@ def _decode_kv4(cache: PagedCache4, q, sel, scale, num_splits, out, lse, want_ls
 def _decode_kv4_checked(cache: PagedCache4, q, sel, scale, num_splits, out, lse, want_lse, ws, stream):
     B, Hq, d = q.shape
     dev = q.device
+    _int32(num_splits, "sparse_decode_attn num_splits")
     kv = kv4_struct(cache, dev)
     if (B, d) != (kv.batch, kv.head_dim):
         raise ValueError("sparse_decode_attn: q is [%d][%d][%d], the 4-bit cache has batch %d and head_dim %d"
@@ -609,6 +617,9 @@ def _plan_append(page_table, seq_lens, new_lens, pool, max_tokens, seq_lens_out,
     _need(new_lens, (B,), torch.int32, dev, "plan_append new_lens")
     _need(pool.free_pages, (pool.free_pages.numel(),), torch.int32, dev, "plan_append pool.free_pages")
     _need(pool.free_count, (1,), torch.int32, dev, "plan_append pool.free_count")
+    _int32(pool.num_pages, "plan_append pool.num_pages")
+    _int32(pool.page_size, "plan_append pool.page_size")
+    _int32(max_tokens, "plan_append max_tokens")
     if seq_lens_out is None:
         seq_lens_out = seq_lens
     else:

@@ -66,6 +66,18 @@ struct Unlocked {
     ~Unlocked() { PyEval_RestoreThread(state); }
 };
 
+// a number of 32 bits; others are left to the Python code's refusals
+bool number(PyObject *o, int32_t *x)
+{
+    const long long v = PyLong_AsLongLong(o);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return false;
+    }
+    *x = (int32_t)v;
+    return v == *x;
+}
+
 // whether the stream (its handle as a Python number) is being captured, or cannot say
 bool captured(PyObject *stream)
 {
@@ -99,13 +111,16 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n)
     const at::Tensor *slo = a[8] == Py_None ? sl : tensor(a[8]), *fco = a[9] == Py_None ? fc : tensor(a[9]);
     const int dev = device_of(pt);
     if (dev < 0 || pt->dim() != 2 || !fp || fp->dim() != 1) return none();
-    const int64_t B = pt->size(0), tokens = PyLong_AsLongLong(a[7]);
+    const int64_t B = pt->size(0);
+    sa_plan_args p{};
+    if (!number(a[5], &p.num_pages) || !number(a[6], &p.page_size) || !number(a[7], &p.max_tokens)) return none();
+    const int64_t tokens = p.max_tokens;
     if (!is(pt, at::kInt, pt->sizes(), dev) || !is(sl, at::kInt, {B}, dev) || !is(add, at::kInt, {B}, dev) ||
         !is(fp, at::kInt, fp->sizes(), dev) || !is(fc, at::kInt, {1}, dev) || !is(slo, at::kInt, {B}, dev) ||
-        !is(fco, at::kInt, {1}, dev) || tokens < 0 || tokens > INT32_MAX)
+        !is(fco, at::kInt, {1}, dev) || tokens < 0 || B > INT32_MAX || pt->size(1) > INT32_MAX ||
+        fp->numel() > INT32_MAX)
         return none();
     at::Tensor cu, pos, slots, seq;
-    sa_plan_args p{};
     p.page_table = static_cast<int32_t *>(ptr(pt));
     p.seq_lens = static_cast<int32_t *>(ptr(sl));
     p.new_lens = static_cast<int32_t *>(ptr(add));
@@ -114,11 +129,8 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n)
     p.seq_lens_out = static_cast<int32_t *>(ptr(slo));
     p.free_count_out = static_cast<int32_t *>(ptr(fco));
     p.batch = (int32_t)B;
-    p.page_size = (int32_t)PyLong_AsLong(a[6]);
     p.max_pages_per_seq = (int32_t)pt->size(1);
-    p.num_pages = (int32_t)PyLong_AsLong(a[5]);
     p.num_free = (int32_t)fp->numel();
-    p.max_tokens = (int32_t)tokens;
     void *ws = PyLong_AsVoidPtr(a[10]);
     const size_t wn = PyLong_AsSize_t(a[11]);
     const auto stream = static_cast<sa_stream_t>(PyLong_AsVoidPtr(a[12]));
@@ -271,14 +283,15 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n)
         s.max_blocks = (int32_t)most;
     }
     const double scale = a[7] == Py_None ? 1.0 / std::sqrt((double)D) : PyFloat_AsDouble(a[7]);
-    const long splits = PyLong_AsLong(a[8]);
+    int32_t splits = 0;
+    if (!number(a[8], &splits)) return none();
     const int lse_too = PyObject_IsTrue(a[9]);
     void *ws = PyLong_AsVoidPtr(a[10]);
     const size_t have = PyLong_AsSize_t(a[11]);
     const auto stream = static_cast<sa_stream_t>(PyLong_AsVoidPtr(a[12]));
     if (PyErr_Occurred()) return nullptr;
     if (splits < 0 || splits > 64) return none();
-    const size_t need = f_decode_bytes(&c, (int32_t)H, (int32_t)splits);
+    const size_t need = f_decode_bytes(&c, (int32_t)H, splits);
     if (need == 0 || need > have) return none();
     const void *queries = ptr(q);
     at::Tensor out, lse;
@@ -287,7 +300,7 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n)
         Unlocked threads;
         out = make({B, H, D}, at::kBFloat16, dev);
         if (lse_too) lse = make({B, H}, at::kFloat, dev);
-        st = f_decode(&c, queries, f32 ? SA_DTYPE_F32 : SA_DTYPE_BF16, (int32_t)H, &s, (float)scale, (int32_t)splits,
+        st = f_decode(&c, queries, f32 ? SA_DTYPE_F32 : SA_DTYPE_BF16, (int32_t)H, &s, (float)scale, splits,
                       out.data_ptr(), lse_too ? static_cast<float *>(lse.data_ptr()) : nullptr, ws, have, stream);
     }
     if (st != SA_OK) return PyLong_FromLong(st);

@@ -1,5 +1,5 @@
-"""Workspaces of the serving-step calls: what a captured graph holds the address
-of stays (CPU)."""
+"""Workspaces of the serving-step calls -- what a captured graph holds the address
+of stays -- and sizes that are refused (CPU)."""
 import weakref
 
 import pytest
@@ -27,3 +27,14 @@ def test_a_captured_workspace_outgrown_is_kept(monkeypatch, again):
     second = weakref.ref(ws.buf)
     ws.at(1 << 18, 7)
     assert second() is None and len(ws._kept) == 1
+
+
+def test_sizes_that_ctypes_would_cut_are_refused():
+    import torch
+    table, lens = torch.zeros((2, 4), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for kw in (dict(num_pages=2 ** 32 + 8), dict(page_size=2 ** 32 + 16), dict(max_tokens=2 ** 31)):
+        a = dict(dict(num_pages=8, page_size=16, max_tokens=4), **kw)
+        pool = sa.PagePool(torch.arange(8, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), a["num_pages"],
+                           a["page_size"])
+        with pytest.raises(ValueError, match="32 bits"):
+            sa.plan_append(table, lens, lens, pool, a["max_tokens"], ws=sa.Workspace("cpu"))
