@@ -83,7 +83,7 @@ def _short(ws: Optional[Workspace], device, stream):
         ws = _default_ws_at.get((device.index, raw))
         if ws is None:
             return None
-    at = ws._raw.get(raw)
+    at = ws._raw.get(raw) if ws._index == device.index else None   # (handles of two devices' streams may be alike)
     return None if at is None else (_fast, at[0], at[1], raw)
 
 
@@ -195,6 +195,7 @@ class Workspace:
     def __init__(self, device=None):
         self.device = device
         self.buf: Optional[torch.Tensor] = None
+        self._index = None   # of buf's device
         self._streams = []
         self._raw = {}   # stream handles in _streams -> (aligned address of buf, bytes from there on)
         self._in_graph = False   # buf was handed to a captured call
@@ -220,6 +221,7 @@ class Workspace:
             n = max(nbytes, 256)
             old = self.buf
             self.buf = self._zeros(n + 256)
+            self._index = self.buf.device.index
             if old is not None and self._in_graph:
                 self._kept.append(old)
             elif old is not None:
@@ -307,7 +309,14 @@ _default_ws_at = {}   # (device index, stream handle) -> the same workspaces
 
 def _scratch(ws: Optional[Workspace], dev: torch.device, stream, nbytes: int):
     """The workspace of a call (the caller's, else the default one of its device
-    and stream) and the stream's handle: (address, bytes, handle)."""
+    and stream) and the stream's handle: (address, bytes, handle).  Raises
+    ValueError for a workspace or a stream of another device."""
+    if stream is not None and stream.device != dev:
+        raise ValueError("the call's tensors are on %s, its stream is on %s" % (dev, stream.device))
+    if ws is not None and (ws.buf is not None or ws.device is not None):
+        on = ws.buf.device if ws.buf is not None else torch.device(ws.device)
+        if on.type != dev.type or on.index not in (None, dev.index):
+            raise ValueError("the call's tensors are on %s, its workspace is on %s" % (dev, on))
     raw = _raw_stream(dev.index) if stream is None else stream.cuda_stream
     if ws is None:
         ws = _default_ws_at.get((dev.index, raw))
