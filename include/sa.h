@@ -431,7 +431,8 @@ SA_API int64_t sa_tier_plan_scratch_ints(int64_t host_pages, int32_t slots);
  * recorded; its tokens get slot -1 (and a fresh table entry -1).  That of an ended
  * sequence stays off the stack; a step that lacks pages without it changes
  * nothing, as above.  (Entries of the stack past the free count may change.)
- *   page_size in {16, 64}, batch <= 4096 (SA_ERR_UNSUPPORTED otherwise).
+ *   page_size in {16, 64}, batch <= 4096, max_tokens and num_free <= 2^30
+ *   (SA_ERR_UNSUPPORTED otherwise).
  *   ws  any workspace of at least 256 bytes (only its status word is used).
  */
 typedef struct {
@@ -572,6 +573,8 @@ SA_API sa_status sa_expand_kv4(const sa_kv4_cache *kv, const int32_t *pages, int
  *     max_blocks pages, is taken for what the longest list holds, so that a capacity
  *     far above that is better given with a count (or made smaller).  The order of
  *     the sums, and so the last bits, go by the count.
+ *   k_cap and max_blocks <= 2^30, batch and num_q_heads <= 65535
+ *   (SA_ERR_UNSUPPORTED otherwise).
  *   ws  workspace of sa_kv4_decode_workspace_bytes(...) bytes
  */
 SA_API sa_status sa_sparse_decode_attn_kv4(const sa_kv4_cache *kv, const void *q, sa_dtype q_dtype,

@@ -462,6 +462,8 @@ sa_status sa_plan_append(const sa_plan_args *p, void *ws, size_t ws_bytes, sa_st
     if (p->page_size != 16 && p->page_size != 64) return SA_ERR_UNSUPPORTED;
     if (p->batch > kPlanMaxBatch || (long long)p->max_pages_per_seq * p->page_size > (1LL << 30))
         return SA_ERR_UNSUPPORTED;
+    // (the kernel counts tokens and pages, a few rows ahead, in 32 bits)
+    if (p->max_tokens > (1 << 30) || p->num_free > (1 << 30)) return SA_ERR_UNSUPPORTED;
     if (!p->free_count || !p->free_count_out || !p->cu_tokens || (p->num_free > 0 && !p->free_pages))
         return SA_ERR_INVALID_ARGUMENT;
     if (p->batch > 0 && (!p->seq_lens || !p->new_lens || !p->seq_lens_out ||
@@ -624,6 +626,8 @@ sa_status sa_sparse_decode_attn_kv4_parts(const sa_kv4_cache *kv, const void *q,
     st = check_decode(kv->batch, kv->num_kv_heads, q, q_dtype, num_q_heads, sel, scale, out, lse_out, &a);
     if (st != SA_OK) return st;
     if (kv->batch > 65535 || num_q_heads > 65535) return SA_ERR_UNSUPPORTED;   // grid dimensions
+    // (list positions, two steps ahead, are counted in 32 bits)
+    if ((a.blocks ? a.max_blocks : a.kcap) > (1 << 30)) return SA_ERR_UNSUPPORTED;
     st = check_ws(ws, ws_bytes, kHeader);
     if (st != SA_OK) return st;
     if (!parts || !aligned(parts, 16) || parts_bytes < sa_kv4_decode_workspace_bytes(kv, num_q_heads, num_splits) - kHeader)
