@@ -26,8 +26,13 @@
 //
 // Ranges.  A query is scaled by a power of two per head so that its largest
 // element lies in [2^9, 2^10): fp16 then holds a bf16 query exactly down to
-// 2^-22 of that element (to 2^-30 of it below), and an fp32 query in two parts
-// to 2^-22.  s_t p_t is scaled by a power of two per half (raised scales
+// 2^-22 of that element (to 2^-30 of it below).  An fp32 query is scaled to [2^10,
+// 2^11) and enters in two parts, the nearest whole numbers, whose products with
+// codes add up without rounding, and the rest in fp16 (2^-23 of the largest
+// element), with sums of their own: the matrix instruction cuts what it adds below
+// its sum's last bits, and with both parts in one sum (the larger in fp16 as it
+// comes) the score of a short list was off by 2e-6, now 2e-7.  Scores are finite
+// while the largest element times |scale| is below 2^112.  s_t p_t is scaled by a power of two per half (raised scales
 // rescale the sums, as a raised maximum does) to at most 2^15: a weight keeps
 // 11 bits down to 2^-21 of the largest scale seen, 8 to 2^-24, and is within
 // 2^-32 of that scale below.  The rounding of a weight times codes of up to 15
@@ -329,6 +334,7 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
 
     // query B fragments: the k-steps' channels follow the order in which widen() hands out a code word (channels i and i + 4)
     uint32_t qb[NQ][NH][CB][2][2];
+    constexpr float kWhole = 12582912.f;              // 1.5 * 2^23
     constexpr float kUnit = 5.9604644775390625e-8f;   // 2^-24
     float qs[2][NH][2];   // 2^-24 sum of the scaled query over each half, heads nh*8 + 2tq + j
     float kf[NH][2];      // scores' factor of those heads: 2^24 scale log2(e) / the query's power of two
@@ -341,36 +347,35 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
             for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(qx[nh][cb][i]));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        const float up = pow2(9 - exponent(top));
+        const float up = pow2((QF32 ? 10 : 9) - exponent(top));
 #pragma unroll
         for (int j = 0; j < 2; ++j) kf[nh][j] = a.qscale / kUnit / __shfl_sync(~0u, up, (2 * tq + j) * 4);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float f = (i & 1) ? up * 0.0625f : up;   // odd nibbles stand for 16 c
-                float y = qx[nh][cb][i] * f, z = qx[nh][cb][i + 4] * f;
-#pragma unroll
-                for (int qi = 0; qi < NQ; ++qi) {
-                    const uint32_t part = pack_pair(y, z);
-                    const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&part));
-                    y -= r.x;
-                    z -= r.y;
-                    qb[qi][nh][cb][i >> 1][i & 1] = part;
+                const float f = (i & 1) ? 0.0625f : 1.f;   // odd nibbles stand for 16 c
+                float y = qx[nh][cb][i] * up, z = qx[nh][cb][i + 4] * up;
+                if (QF32) {
+                    const float u = y + kWhole - kWhole, v = z + kWhole - kWhole;   // to whole numbers
+                    qb[0][nh][cb][i >> 1][i & 1] = pack_pair(u * f, v * f);
+                    y -= u;
+                    z -= v;
                 }
+                qb[NQ - 1][nh][cb][i >> 1][i & 1] = pack_pair(y * f, z * f);
             }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            float sum[2][4] = {};   // (of the parts on their own, as the scores below)
 #pragma unroll
             for (int cb = half * CBH; cb < (half + 1) * CBH; ++cb)
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                     for (int qi = 0; qi < NQ; ++qi)
-                        mma(sum, kOnes, kOnes, kSixteens, kSixteens, qb[qi][nh][cb][ks][0], qb[qi][nh][cb][ks][1]);
-            qs[half][nh][0] = sum[0] * kUnit;
-            qs[half][nh][1] = sum[1] * kUnit;
+                        mma(sum[qi], kOnes, kOnes, kSixteens, kSixteens, qb[qi][nh][cb][ks][0], qb[qi][nh][cb][ks][1]);
+            qs[half][nh][0] = (sum[0][0] + sum[1][0]) * kUnit;
+            qs[half][nh][1] = (sum[0][1] + sum[1][1]) * kUnit;
         }
     }
     // O^T fragments: o[cb][j][nh]: rows gq / gq + 8 are channels cb*32 + 4gq + 2j / + 1, columns heads 2tq, 2tq + 1
@@ -423,6 +428,7 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
             for (int c2 = 0; c2 < CB; c2 += 2) {
                 // matrices: rows 0-7 / 8-15 of column block c2, then of c2 + 1
                 uint32_t w[4];
+                float low[NH][4];   // QF32: the sums of the query's second part
                 ldsm4(quad0 + at + t * 16 * REC + c2 * 16, w);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
@@ -436,13 +442,19 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
                         for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
                             for (int qi = 0; qi < NQ; ++qi) {
-                                if (cb == half * CBH && ks == 0 && qi == 0)
-                                    mma0(sc[t][half][nh], f0[0], f1[0], f0[1], f1[1], qb[0][nh][cb][0][0],
-                                         qb[0][nh][cb][0][1]);
+                                float(&sum)[4] = qi ? low[nh] : sc[t][half][nh];
+                                if (cb == half * CBH && ks == 0)
+                                    mma0(sum, f0[0], f1[0], f0[1], f1[1], qb[qi][nh][cb][0][0], qb[qi][nh][cb][0][1]);
                                 else
-                                    mma(sc[t][half][nh], f0[2 * ks], f1[2 * ks], f0[2 * ks + 1], f1[2 * ks + 1],
+                                    mma(sum, f0[2 * ks], f1[2 * ks], f0[2 * ks + 1], f1[2 * ks + 1],
                                         qb[qi][nh][cb][ks][0], qb[qi][nh][cb][ks][1]);
                             }
+                    if (QF32 && cb + 1 == (half + 1) * CBH) {
+#pragma unroll
+                        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) sc[t][half][nh][i] += low[nh][i];
+                    }
                 }
             }
         if (PACK) {
