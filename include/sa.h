@@ -407,6 +407,7 @@ SA_API int64_t sa_tier_plan_scratch_ints(int64_t host_pages, int32_t slots);
  *                     ceil((n + new) / P) - ceil(n / P) fresh pages;
  *   new_lens[b] == -1 the sequence has ended: its ceil(n / P) pages are free
  *                     again and its length becomes 0 (its table row is left).
+ * A page belongs to one sequence: one that two ended sequences hold is freed twice.
  * Freed pages are pushed onto the stack in (sequence, page) order; then the
  * fresh pages are popped in the same order.  Table entries past a sequence's
  * pages are left as they were.

@@ -710,7 +710,8 @@ def _rope_append(cache, q, k, v, positions, slots, inv_freq, q_weight, k_weight,
     if d != kv.head_dim:
         raise ValueError("rope_append: head_dim %d, the cache's is %d" % (d, kv.head_dim))
     if q_out is not None and q_out is not q:
-        if q_out.dtype != torch.bfloat16 or tuple(q_out.shape) != (T, Hq, d) or q_out.device != dev or                 q_out.stride(2) != 1 or q_out.stride(1) != d or q_out.stride(0) % 8 or q_out.data_ptr() % 16:
+        if q_out.dtype != torch.bfloat16 or tuple(q_out.shape) != (T, Hq, d) or q_out.device != dev or \
+                q_out.stride(2) != 1 or q_out.stride(1) != d or q_out.stride(0) % 8 or q_out.data_ptr() % 16:
             raise ValueError("rope_append q_out: need a bf16 [T][Hq][d] tensor on %s with contiguous heads" % dev)
     src, qs = _rows(q, "q", (T, Hq, d), dev)
     if q_out is q and src is not q:

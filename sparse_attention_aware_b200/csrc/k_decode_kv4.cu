@@ -19,7 +19,7 @@
 // 4-7 is 16 c 2^-24, and fp16 products are exact, so eight codes cost one
 // shift and four masks.  The 16 goes into the query (a sixteenth of those
 // channels) or out of the sums (those rows of O), the 2^24 into the factors.
-// Before, at 32 sequences x 8 kv heads, 435 MB of records: 146 us with bf16
+// Before, at 32 sequences x 8 kv heads of up to 16384 tokens: 146 us with bf16
 // numbers 1 + c/16 (one logic operation and one shift a pair, all on the
 // integer pipe), 118 us with fp16 numbers c - 8 (a mask-or and an fma a pair),
 // 95 us with the codes as they are, all else equal.
@@ -63,13 +63,17 @@
 // 142.5 -> 138).
 //
 // Measured (B200, 6.55 TB/s copy): every page of 32 sequences of up to 16384
-// tokens, 32 heads on 8 kv heads (435 MB) 80 us, 0.83 of HBM; 1024 lists of 4096
-// of 65536 tokens 138 us (0.60 by the rows' own bytes; a row's 144 bytes touch
-// 192 in 64-byte pieces, and by those it is 0.88); a masked step of 4 sequences
-// 10 us, 256 of 4096 tokens of 4 heads 4.8 us.  The copies alone take 67 and 134
+// tokens, 32 heads on 8 kv heads (421 MB) 82 us, 0.79 of HBM; 1024 lists of 4096
+// of 65536 tokens 139 us (0.56 by the 506 MB of distinct rows and lists; 794 MB are
+// read, since a row's 144 bytes touch 192 in 64-byte pieces and rows that heads share
+// come again, and by those it is 0.87); a masked step of 4 sequences 10 us, 256 of
+// 4096 tokens of 4 heads, fp32 queries, 5.1 us.  The copies alone take 67 and 134
 // us, the arithmetic alone 76 and 123: about 230 instructions per 16 rows (267 with
 // a list), of which widening the codes is a third, with 12 to 16 warps an SM.  Short
 // calls are bound by the dependent trips length -> entry -> page -> rows -> merge.
+// Farther from their floors: groups of 5 to 8 heads (16 x 8 groups of up to 16384
+// tokens 54 us, 0.67 of HBM) and of 9 to 16 (8 x 4 of up to 65536 81 us, 0.44: one
+// tile at a time, 8 warps an SM); fp32 queries (the first case 95 us).
 //
 // Measured and not kept (whole context, 81 us at that stage): a page segment by
 // bulk copies 88; the next tiles' scores between a tile's weights and its products

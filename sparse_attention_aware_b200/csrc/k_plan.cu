@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_append(const PlanArgs a)
 
 cudaError_t launch_plan(const PlanArgs &a, cudaStream_t s)
 {
-    // a step's few tokens need one CTA (4.4 us for 32); 131072 take 11.7 us with
-    // 16 CTAs and 14.8 with 8
+    // a step's few tokens need one CTA (4.4 us for 32); 131072 take 10.3 us with
+    // 16 CTAs and 13.7 with 8
     const int ctas = a.max_tokens > 32 * kPlanThreads ? 16 : a.max_tokens > 4 * kPlanThreads || a.B > kPlanThreads ? 8 : 1;
     auto kern = ctas == 1 ? k_plan_append<true> : k_plan_append<false>;
     const size_t smem = (size_t)(4 * a.B + 1) * sizeof(int);
