@@ -56,11 +56,15 @@ def fastcall_fits() -> bool:
         return False
 
 
+def _fastcall_fresh() -> bool:
+    deps = [FAST_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return fastcall_fits() and all(os.path.getmtime(p) <= os.path.getmtime(FAST) for p in deps)
+
+
 def build_fastcall(force: bool = False) -> str:
     """The short calls of the binding, a Python module against torch's own
     libraries (already loaded by whoever imports it)."""
-    deps = [FAST_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and fastcall_fits() and all(os.path.getmtime(p) <= os.path.getmtime(FAST) for p in deps):
+    if not force and _fastcall_fresh():
         return FAST
     import torch
     base = os.path.dirname(torch.__file__)
@@ -83,7 +87,7 @@ def _try_fastcall(force: bool) -> None:
     try:
         build_fastcall(force)
     except Exception as e:   # no compiler, headers or torch libraries, or not fitting ones
-        if os.path.exists(FAST):
+        if os.path.exists(FAST) and not _fastcall_fresh():
             os.remove(FAST)
         warnings.warn("the binding's native calls were not built: %s" % e, RuntimeWarning)
 

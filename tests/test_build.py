@@ -75,3 +75,16 @@ def test_native_calls_that_do_not_fit_are_not_loaded(monkeypatch, tmp_path, cont
 def test_the_built_native_calls_fit():
     B.build()
     assert B.fastcall_fits()
+
+
+def test_a_forced_build_that_fails_leaves_native_calls_that_fit(monkeypatch, place):
+    ran, at = place
+    (at / "_fastcall.so").write_bytes(B._made_for().encode())
+
+    def fail(force=False):
+        raise FileNotFoundError("g++")
+
+    monkeypatch.setattr(B, "build_fastcall", fail)
+    with pytest.warns(RuntimeWarning, match="native calls"):
+        B.build(force=True)
+    assert B.fastcall_fits()
