@@ -13,6 +13,7 @@ import functools
 import inspect
 import math
 import operator
+import threading
 import warnings
 from typing import Optional, Sequence
 
@@ -70,9 +71,9 @@ _fast = False   # False: not looked for yet
 
 
 def _short(ws: Optional[Workspace], device, stream):
-    """(native calls, workspace address, bytes, stream handle) if a call may go
-    the short way: it is on torch's current stream, with a workspace that has
-    served that stream before."""
+    """(native calls, workspace address, bytes, stream handle, what keeps the
+    buffer) if a call may go the short way: it is on torch's current stream, with
+    a workspace that has served that stream before."""
     global _fast
     if _fast is False:
         _fast = _load_fast()
@@ -84,7 +85,7 @@ def _short(ws: Optional[Workspace], device, stream):
         if ws is None:
             return None
     at = ws._raw.get(raw) if ws._index == device.index else None   # (handles of two devices' streams may be alike)
-    return None if at is None else (_fast, at[0], at[1], raw)
+    return None if at is None else (_fast, at[0], at[1], raw, at)
 
 
 def _raw_stream(index: int) -> int:
@@ -190,14 +191,20 @@ class Workspace:
     captured call was handed is kept instead: every replay of that graph writes
     to it again, and ``status`` reads it too.  A workspace that is captured must
     outlive its graphs; one that is made by a captured call is cleared by every
-    replay of that call's graph."""
+    replay of that call's graph.
+
+    What gives a call its address keeps the buffer as well, and the call holds it
+    until it has launched: another thread's call on the same stream may replace
+    the buffer in between, but its memory is let go, behind the launch, by the
+    last call that holds it."""
 
     def __init__(self, device=None):
         self.device = device
         self.buf: Optional[torch.Tensor] = None
         self._index = None   # of buf's device
         self._streams = []
-        self._raw = {}   # stream handles in _streams -> (aligned address of buf, bytes from there on)
+        self._raw = {}   # stream handles in _streams -> (aligned address of buf, bytes from there on, buf)
+        self._grow = threading.Lock()
         self._in_graph = False   # buf was handed to a captured call
         self._kept = []          # outgrown buffers that were
 
@@ -205,42 +212,63 @@ class Workspace:
         return torch.zeros(n, dtype=torch.uint8, device=self.device or "cuda")
 
     def at(self, nbytes: int, raw: int, stream=None):
-        """``aligned`` for a call on the stream of handle ``raw``, without asking
-        torch for its stream object when the buffer has served it before."""
+        """(address, bytes, what keeps the buffer) for a call on the stream of handle
+        ``raw``, without asking torch for its stream object when the buffer has
+        served it before."""
         got = self._raw.get(raw)
         if got is not None and got[1] >= nbytes:
-            self._in_graph = self._in_graph or _capturing()
+            if _capturing():
+                self._captured(got[2])
             return got
-        ptr, n = self.aligned(nbytes + 256, stream)
-        if self.buf.numel() and raw not in self._raw:
-            self._raw[raw] = (ptr.value, n)
-        return ptr.value, n
+        buf = self.get(nbytes + 256, stream)
+        at = _aligned(buf)
+        got = at, buf.numel() - (at - buf.data_ptr()), buf
+        with self._grow:
+            if self.buf is buf:
+                self._raw[raw] = got
+        return got
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
-        if self.buf is None or self.buf.numel() < nbytes:
-            n = max(nbytes, 256)
-            old = self.buf
-            self.buf = self._zeros(n + 256)
-            self._index = self.buf.device.index
-            if old is not None and self._in_graph:
-                self._kept.append(old)
-            elif old is not None:
-                for s in self._streams:
-                    old.record_stream(s)
-            self._streams = []
-            self._raw = {}
-            self._in_graph = False
-        self._in_graph = self._in_graph or _capturing()
-        if self.buf.device.type == "cuda":
-            s = stream if stream is not None else torch.cuda.current_stream(self.buf.device)
+        buf = self.buf
+        if buf is None or buf.numel() < nbytes:
+            with self._grow:
+                buf = self.buf
+                if buf is None or buf.numel() < nbytes:
+                    buf = self._zeros(max(nbytes, 256) + 256)
+                    if self.buf is not None and self._in_graph:
+                        self._kept.append(self.buf)
+                    elif self.buf is not None:
+                        for s in self._streams:
+                            self.buf.record_stream(s)
+                    self._streams = []
+                    self._raw = {}
+                    self._in_graph = False
+                    self._index = buf.device.index
+                    self.buf = buf
+        if _capturing():
+            self._captured(buf)
+        if buf.device.type == "cuda":
+            s = stream if stream is not None else torch.cuda.current_stream(buf.device)
             if all(s != x for x in self._streams):
                 self._streams.append(s)
-        return self.buf
+                if self.buf is not buf:   # replaced since, and released for the streams that were known
+                    buf.record_stream(s)
+        return buf
+
+    def _captured(self, buf: torch.Tensor) -> None:
+        """``buf`` is handed to a captured call."""
+        with self._grow:
+            if self.buf is buf:
+                self._in_graph = True
+            elif all(buf is not x for x in self._kept):
+                self._kept.append(buf)
 
     def aligned(self, nbytes: int, stream=None):
         buf = self.get(nbytes, stream)
         at = _aligned(buf)
-        return ctypes.c_void_p(at), buf.numel() - (at - buf.data_ptr())
+        ptr = ctypes.c_void_p(at)
+        ptr.held = buf
+        return ptr, buf.numel() - (at - buf.data_ptr())
 
     def status(self, stream=None):
         """Synchronise and return (status, detail) recorded by kernels (then cleared)."""
@@ -309,8 +337,8 @@ _default_ws_at = {}   # (device index, stream handle) -> the same workspaces
 
 def _scratch(ws: Optional[Workspace], dev: torch.device, stream, nbytes: int):
     """The workspace of a call (the caller's, else the default one of its device
-    and stream) and the stream's handle: (address, bytes, handle).  Raises
-    ValueError for a workspace or a stream of another device."""
+    and stream) and the stream's handle: (address, bytes, handle, what keeps the
+    buffer).  Raises ValueError for a workspace or a stream of another device."""
     if stream is not None and stream.device != dev:
         raise ValueError("the call's tensors are on %s, its stream is on %s" % (dev, stream.device))
     if ws is not None and (ws.buf is not None or ws.device is not None):
@@ -322,8 +350,8 @@ def _scratch(ws: Optional[Workspace], dev: torch.device, stream, nbytes: int):
         ws = _default_ws_at.get((dev.index, raw))
         if ws is None:
             ws = _default_ws_at[(dev.index, raw)] = _ws(None, dev, stream)
-    ptr, n = ws.at(nbytes, raw, stream)
-    return ptr, n, raw
+    at = ws.at(nbytes, raw, stream)
+    return at[0], at[1], raw, at
 
 
 def _ws(ws: Optional[Workspace], device, stream=None) -> Workspace:
@@ -523,7 +551,7 @@ def _decode_kv4(cache: PagedCache4, q, sel, scale, num_splits, out, lse, want_ls
         if way is not None:
             tok = isinstance(sel, TokenSelection)
             if tok or isinstance(sel, BlockSelection):
-                fast, wp, wn, raw = way
+                fast, wp, wn, raw, _ = way
                 got = fast.decode(cache.kv, cache.page_table, cache.seq_lens, q, sel.idx if tok else sel.blocks,
                                   sel.count if tok else sel.block_counts, L.SEL_TOKENS if tok else L.SEL_BLOCKS, scale,
                                   num_splits, want_lse, wp, wn, raw)
@@ -561,12 +589,12 @@ def _decode_kv4_checked(cache: PagedCache4, q, sel, scale, num_splits, out, lse,
             None if lse is None else lse.data_ptr())
     if ws is None and _capturing():
         # graphs may be replayed side by side: each call keeps its parts in its graph's own memory
-        wp, wn, raw = _scratch(None, dev, stream, 256)
+        wp, wn, raw, _ = _scratch(None, dev, stream, 256)
         parts = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
         _check(lib.sa_sparse_decode_attn_kv4_parts(*call, parts.data_ptr(), parts.numel(), wp, wn, raw),
                "sa_sparse_decode_attn_kv4_parts")
         return out, lse
-    wp, wn, raw = _scratch(ws, dev, stream, need)
+    wp, wn, raw, _ = _scratch(ws, dev, stream, need)
     _check(lib.sa_sparse_decode_attn_kv4(*call, wp, wn, raw), "sa_sparse_decode_attn_kv4")
     return out, lse
 
@@ -603,7 +631,7 @@ def plan_append(page_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torc
     if plan is None:
         way = _short(ws, page_table.device, stream)
         if way is not None:
-            fast, wp, wn, raw = way
+            fast, wp, wn, raw, _ = way
             got = fast.plan(page_table, seq_lens, new_lens, pool.free_pages, pool.free_count, pool.num_pages,
                             pool.page_size, max_tokens, seq_lens_out, free_count_out, wp, wn, raw)
             if got is not None:
@@ -649,7 +677,7 @@ def _plan_append(page_table, seq_lens, new_lens, pool, max_tokens, seq_lens_out,
                     plan.cu_tokens.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr(),
                     plan.seq_ids.data_ptr(), B, pool.page_size, mp, pool.num_pages, pool.free_pages.numel(),
                     max_tokens)
-    wp, wn, raw = _scratch(ws, dev, stream, 256)
+    wp, wn, raw, _ = _scratch(ws, dev, stream, 256)
     _check(L.load().sa_plan_append(ctypes.byref(a), wp, wn, raw), "sa_plan_append")
     return plan
 
@@ -685,7 +713,7 @@ def rope_append(cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positi
     if q_out is None:
         way = _short(ws, q.device, stream)
         if way is not None:
-            fast, wp, wn, raw = way
+            fast, wp, wn, raw, _ = way
             four = isinstance(cache, PagedCache4)
             got = fast.append(cache.kv if four else cache.k, None if four else cache.v, cache.page_table,
                               cache.seq_lens, q, k, v, positions, slots, inv_freq, q_weight, k_weight, eps, interleaved,
@@ -740,7 +768,7 @@ def _rope_append(cache, q, k, v, positions, slots, inv_freq, q_weight, k_weight,
                       None if rot == 0 else inv_freq.data_ptr(), None if q_weight is None else q_weight.data_ptr(),
                       None if k_weight is None else k_weight.data_ptr(), L.DTYPE_F32 if wt == torch.float32 else
                       L.DTYPE_BF16, eps, T, Hq, rot, int(interleaved))
-    wp, wn, raw = _scratch(ws, dev, stream, 256)
+    wp, wn, raw, _ = _scratch(ws, dev, stream, 256)
     lib = L.load()
     fn = lib.sa_rope_append_kv4 if four else lib.sa_rope_append
     _check(fn(ctypes.byref(kv), ctypes.byref(a), wp, wn, raw),
@@ -756,7 +784,7 @@ def expand_kv4(cache: PagedCache4, pages: torch.Tensor, k: Optional[torch.Tensor
     if k is None and v is None:
         way = _short(ws, pages.device, stream)
         if way is not None:
-            fast, wp, wn, raw = way
+            fast, wp, wn, raw, _ = way
             got = fast.expand(cache.kv, cache.page_table, cache.seq_lens, pages, wp, wn, raw)
             if got is not None:
                 if isinstance(got, int):
@@ -779,7 +807,7 @@ def _expand_kv4(cache, pages, k, v, ws, stream=None):
         v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     else:
         _need(v, shape, torch.bfloat16, dev, "expand_kv4 v")
-    wp, wn, raw = _scratch(ws, dev, stream, 256)
+    wp, wn, raw, _ = _scratch(ws, dev, stream, 256)
     _check(L.load().sa_expand_kv4(ctypes.byref(kv), pages.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(), wp, wn,
                                   raw), "sa_expand_kv4")
     return k, v

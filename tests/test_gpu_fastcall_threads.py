@@ -2,6 +2,7 @@
 import subprocess
 import threading
 import time
+import weakref
 
 import pytest
 import torch
@@ -72,3 +73,26 @@ def test_other_threads_run_while_a_call_waits(cuda_dev, slow):
     finally:
         done.set()
         t.join()
+
+
+def test_a_replaced_buffer_outlives_the_native_call_that_uses_it(cuda_dev, slow):
+    """Another thread's call outgrows the workspace while a native call on it waits."""
+    i32 = dict(dtype=torch.int32, device=cuda_dev)
+    table, lens = torch.zeros((2, 3), **i32), torch.zeros(2, **i32)
+    pool = sa.PagePool.full(6, 16, cuda_dev)
+    ws = sa.Workspace(cuda_dev)
+    ws.at(1 << 12, torch.cuda.current_stream(cuda_dev).cuda_stream)
+    first, seen = weakref.ref(ws.buf), []
+
+    def grow():
+        time.sleep(0.1)                  # the call below waits 0.3 s
+        ws.get(1 << 20)
+        seen.append((ws.buf is not first(), first() is not None, time.monotonic()))
+
+    t = threading.Thread(target=grow)
+    t.start()
+    with pytest.raises(sa.SAError):
+        sa.plan_append(table, lens, lens, pool, 4, ws=ws)
+    done = time.monotonic()
+    t.join()
+    assert seen[0][:2] == (True, True) and seen[0][2] < done
