@@ -566,12 +566,12 @@ SA_API sa_status sa_expand_kv4(const sa_kv4_cache *kv, const int32_t *pages, int
 /* ------------------------------------------------------------------------ */
 /*
  * What sa_sparse_decode_attn computes, over the values a 4-bit cache stands
- * for: same selections, outputs and errors.  Scores are accumulated in fp32 (an
- * fp32 query enters to 2^-23 of its head's largest element, or to 2^-140 where all
- * are below 2^-117); they are finite while that element times |scale| is below
- * 2^112.  A softmax weight times its row's scale enters the P.V product as fp16,
- * scaled by a power of two.  A selected row that was stored as NaN makes the outputs
- * of its heads NaN.
+ * for: same selections, outputs and errors.  Scores are accumulated in fp32, to
+ * which a bf16 query's elements contribute down to 2^-18 of their head's largest,
+ * an fp32 query's to 2^-23 (to 2^-140 where all are below 2^-117); they are finite
+ * while the largest element times |scale| is below 2^112.  A softmax weight times
+ * its row's scale enters the P.V product as fp16, scaled by a power of two.  A
+ * selected row that was stored as NaN makes the outputs of its heads NaN.
  *   num_splits in [0, 64]; 0 lets the library choose from the sizes: k_cap, or
  *     max_blocks pages, is taken for what the longest list holds, so that a capacity
  *     far above that is better given with a count (or made smaller).  The order of

@@ -13,30 +13,37 @@
 //   q . k = sum over halves of  s (q . c) + z sum(q)
 //   sum_t p_t v_t = sum_t p'_t c_t + sum_t p_t z_t,     p'_t = fp16(s_t p_t)
 // so scales and zeros act outside the products, and sum(q) comes from a
-// product with ones of the very fp16 parts of q that the first product uses.
-// The codes enter the matrix instruction as they are: a nibble alone in the
-// low bits of a 16-bit word is the subnormal fp16 number c 2^-24, one in bits
-// 4-7 is 16 c 2^-24, and fp16 products are exact, so eight codes cost one
-// shift and four masks.  The 16 goes into the query (a sixteenth of those
-// channels) or out of the sums (those rows of O), the 2^24 into the factors.
+// product with ones of the very parts of q that the first product uses.
+// The codes enter the matrix instruction as they are: a nibble alone in the low
+// bits of a 16-bit word is the subnormal number c 2^-24 in fp16 and c 2^-133 in
+// bf16, one in bits 4-7 is 16 times that (in bf16 half of them are past the
+// subnormals, where the numbers go on in the same steps), and the products are
+// exact, so eight codes cost one shift and four masks.  The 16 goes into the query
+// (a sixteenth of those channels) or out of the sums (those rows of O), the power
+// of two into the factors.
 // Before, at 32 sequences x 8 kv heads of up to 16384 tokens: 146 us with bf16
 // numbers 1 + c/16 (one logic operation and one shift a pair, all on the
 // integer pipe), 118 us with fp16 numbers c - 8 (a mask-or and an fma a pair),
 // 95 us with the codes as they are, all else equal.
 //
-// Ranges.  A query is scaled by a power of two per head so that its largest
-// element lies in [2^9, 2^10): fp16 then holds a bf16 query exactly down to
-// 2^-22 of that element (to 2^-30 of it below).  An fp32 query is scaled to [2^10,
-// 2^11) and enters in two parts, the nearest whole numbers, whose products with
-// codes add up without rounding, and the rest in fp16 (2^-23 of the largest
-// element), with sums of their own: the matrix instruction cuts what it adds below
-// its sum's last bits, and with both parts in one sum (the larger in fp16 as it
-// comes) the score of a short list was off by 2e-6, now 2e-7.  Scores are finite
-// while the largest element times |scale| is below 2^112.  s_t p_t is scaled by a power of two per half (raised scales
+// Ranges.  The matrix instruction lines products up by their operands' exponents,
+// of which a subnormal's is the type's least, and drops what then lies below the
+// 24 bits of fp32: a code of 1 loses products below 2^-15 of the largest one's in
+// fp16, 2^-18 in bf16.  So a bf16 query meets its keys' codes as bf16, exactly and
+// scaled by a power of two per head; only elements below 2^-10 of the head's
+// largest lose bits (in fp16, scores of queries with a few large channels were off
+// by up to 6e-5 of themselves, now 1.0 to 1.7 times a plain fp32 form's error on
+// Gaussian ones).  Codes times 16 by a bf16 product first would keep 2^-22, at 2%
+// more time.  An fp32 query is scaled to a largest element in [2^10, 2^11) and
+// enters as fp16 in two parts: the nearest whole numbers, whose products with codes
+// add up without any loss, and the rest, to 2^-23 of the largest element, with sums
+// of their own.  Scores are finite while the largest element times |scale| is below
+// 2^112.  s_t p_t is scaled by a power of two per half (raised scales
 // rescale the sums, as a raised maximum does) to at most 2^15: a weight keeps
 // 11 bits down to 2^-21 of the largest scale seen, 8 to 2^-24, and is within
-// 2^-32 of that scale below.  The rounding of a weight times codes of up to 15
-// steps stays below that of the bf16 output.
+// 2^-32 of that scale below.  Its rounding acts on scale times code, about 2.7
+// times the value where values are spread around 0: next to the rounding of the bf16
+// output it makes the error 2 to 5% larger than that of weights in fp32.
 //
 // One CTA = (split, kv head and up to 16 of its query heads -- or one query
 // head for token lists --, sequence), kDW warps that run independently until
@@ -136,25 +143,41 @@ __device__ __forceinline__ uint32_t movm(uint32_t x)
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// D (16x8 fp32) = A (16x16 fp16, row) * B (16x8 fp16, col)
+// D (16x8 fp32) = A (16x16, row) * B (16x8, col), fp16 or bf16
+template <bool BF>
 __device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                      uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    if (BF)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// D (16x8 fp32) += A (16x16 fp16, row) * B (16x8 fp16, col)
+// D += A * B
+template <bool BF>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if (BF)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // the 8 codes of a word as 4 fp16 pairs: f[i] holds nibble i of the low half
@@ -178,10 +201,19 @@ __device__ __forceinline__ void widen_bytes(uint32_t w, uint32_t (&f)[4])
     f[0] = w & 0x000f000fu;
     f[2] = f[3] & 0x000f000fu;
 }
-constexpr uint32_t kOnes = 0x3c003c00u, kSixteens = 0x4c004c00u;   // fp16 pairs
+// pairs of 1 and of 16
+template <bool BF>
+constexpr uint32_t kOnes = BF ? 0x3f803f80u : 0x3c003c00u;
+template <bool BF>
+constexpr uint32_t kSixteens = BF ? 0x41804180u : 0x4c004c00u;
 
+template <bool BF = false>
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi)
 {
+    if (BF) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&p);
+    }
     const __half2 p = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
 }
@@ -338,10 +370,12 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
 
     // query B fragments: the k-steps' channels follow the order in which widen() hands out a code word (channels i and i + 4)
     uint32_t qb[NQ][NH][CB][2][2];
-    constexpr float kWhole = 12582912.f;              // 1.5 * 2^23
-    constexpr float kUnit = 5.9604644775390625e-8f;   // 2^-24
-    float qs[2][NH][2];   // 2^-24 sum of the scaled query over each half, heads nh*8 + 2tq + j
-    float kf[NH][2];      // scores' factor of those heads: 2^24 scale log2(e) / the query's power of two
+    constexpr float kWhole = 12582912.f;   // 1.5 * 2^23
+    constexpr bool BF = !QF32;             // type of the products with keys
+    constexpr int kTop = BF ? 118 : 10;    // the scaled query's largest element is in [2^kTop, 2^(kTop + 1))
+    constexpr int kUnit = BF ? 133 : 24;   // a code c stands as c 2^-kUnit
+    float qs[2][NH][2];   // 2^-kUnit sum of the scaled query over each half, heads nh*8 + 2tq + j
+    float kf[NH][2];      // scores' factor of those heads: 2^kUnit scale log2(e) / the query's power of two
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
         float top = 0.f;
@@ -351,9 +385,9 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
             for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(qx[nh][cb][i]));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        const float up = pow2((QF32 ? 10 : 9) - exponent(top));
+        const float up = pow2(kTop - exponent(top));
 #pragma unroll
-        for (int j = 0; j < 2; ++j) kf[nh][j] = a.qscale / kUnit / __shfl_sync(~0u, up, (2 * tq + j) * 4);
+        for (int j = 0; j < 2; ++j) kf[nh][j] = a.qscale * pow2(kUnit - kUnit / 2) * (pow2(kUnit / 2) / __shfl_sync(~0u, up, (2 * tq + j) * 4));
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
@@ -362,11 +396,11 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
                 float y = qx[nh][cb][i] * up, z = qx[nh][cb][i + 4] * up;
                 if (QF32) {
                     const float u = y + kWhole - kWhole, v = z + kWhole - kWhole;   // to whole numbers
-                    qb[0][nh][cb][i >> 1][i & 1] = pack_pair(u * f, v * f);
+                    qb[0][nh][cb][i >> 1][i & 1] = pack_pair<BF>(u * f, v * f);
                     y -= u;
                     z -= v;
                 }
-                qb[NQ - 1][nh][cb][i >> 1][i & 1] = pack_pair(y * f, z * f);
+                qb[NQ - 1][nh][cb][i >> 1][i & 1] = pack_pair<BF>(y * f, z * f);
             }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -377,9 +411,11 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
                 for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                     for (int qi = 0; qi < NQ; ++qi)
-                        mma(sum[qi], kOnes, kOnes, kSixteens, kSixteens, qb[qi][nh][cb][ks][0], qb[qi][nh][cb][ks][1]);
-            qs[half][nh][0] = (sum[0][0] + sum[1][0]) * kUnit;
-            qs[half][nh][1] = (sum[0][1] + sum[1][1]) * kUnit;
+                        mma<BF>(sum[qi], kOnes<BF>, kOnes<BF>, kSixteens<BF>, kSixteens<BF>, qb[qi][nh][cb][ks][0],
+                                qb[qi][nh][cb][ks][1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                qs[half][nh][j] = (sum[0][j] + sum[1][j]) * pow2(-(kUnit / 2)) * pow2(-(kUnit - kUnit / 2));
         }
     }
     // O^T fragments: o[cb][j][nh]: rows gq / gq + 8 are channels cb*32 + 4gq + 2j / + 1, columns heads 2tq, 2tq + 1
@@ -448,10 +484,11 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
                             for (int qi = 0; qi < NQ; ++qi) {
                                 float(&sum)[4] = qi ? low[nh] : sc[t][half][nh];
                                 if (cb == half * CBH && ks == 0)
-                                    mma0(sum, f0[0], f1[0], f0[1], f1[1], qb[qi][nh][cb][0][0], qb[qi][nh][cb][0][1]);
+                                    mma0<BF>(sum, f0[0], f1[0], f0[1], f1[1], qb[qi][nh][cb][0][0],
+                                             qb[qi][nh][cb][0][1]);
                                 else
-                                    mma(sum, f0[2 * ks], f1[2 * ks], f0[2 * ks + 1], f1[2 * ks + 1],
-                                        qb[qi][nh][cb][ks][0], qb[qi][nh][cb][ks][1]);
+                                    mma<BF>(sum, f0[2 * ks], f1[2 * ks], f0[2 * ks + 1], f1[2 * ks + 1],
+                                            qb[qi][nh][cb][ks][0], qb[qi][nh][cb][ks][1]);
                             }
                     if (QF32 && cb + 1 == (half + 1) * CBH) {
 #pragma unroll
@@ -595,7 +632,7 @@ __global__ void __launch_bounds__(kDThreads, kOcc<NH, QF32, TOKENS>) k_decode_kv
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int nh = 0; nh < NH; ++nh)
-                            mma(o[cb][j][nh], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], pb[t][half][nh][0],
+                            mma<false>(o[cb][j][nh], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], pb[t][half][nh][0],
                                 pb[t][half][nh][1]);
                 }
             }
