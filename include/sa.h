@@ -473,8 +473,9 @@ SA_API sa_status sa_plan_append(const sa_plan_args *args, void *ws, size_t ws_by
  * A code c stands for zero + scale * c.  Storing a half row x: zero = bf16(min
  * x), scale = bf16((max x - min x) / 15), each by way of fp32, and c = (x -
  * zero) / scale to the nearest whole number, ties to even, in [0, 15] (0 where
- * scale is 0).  A half row with a value that is not finite, or whose scale or
- * zero would not be, is stored with scale and zero NaN.
+ * scale is 0).  (A minimum of 0 may be stored as 0 or -0 where the row holds both.)
+ * A half row with a value that is not finite, or whose scale or zero would not be,
+ * is stored with scale and zero NaN.
  * Supported as for sa_kv_cache; also num_pages * num_kv_heads * page_size <
  * 2^32 - 1 (SA_ERR_UNSUPPORTED otherwise).  kv is 16-byte aligned.
  */

@@ -192,3 +192,38 @@ def test_a_default_workspace_grown_by_a_captured_call(cuda_dev):
     st, det = sa.device_status(cuda_dev)
     assert st == DEVICE_FAULT and det[1] == 5
     del graph
+
+
+def test_a_default_workspace_outgrown_after_the_capture(cuda_dev):
+    """Captured without a workspace, then a call on that stream that needs more: a
+    replay's record reaches no other tensor, and is read."""
+    s = _plan_inputs(cuda_dev)
+    i32 = dict(dtype=torch.int32, device=cuda_dev)
+    g = torch.Generator().manual_seed(3)
+    c = sa.PagedCache4(R.random_records(g, 6, 2, 16, 64).to(cuda_dev), torch.arange(6, **i32).view(2, 3),
+                       torch.tensor([40, 20], **i32))
+    q = torch.randn(2, 16, 64, generator=g).bfloat16().to(cuda_dev)
+    blocks, cnt = R.pack_entries([R.entries_of([(0, n)], n, 16) for n in (40, 20)])
+    sel = sa.BlockSelection(blocks.to(cuda_dev), cnt.to(cuda_dev))
+    stream = torch.cuda.Stream(cuda_dev)
+    stream.wait_stream(torch.cuda.current_stream(cuda_dev))
+    with torch.cuda.stream(stream):
+        sa.plan_append(**s)
+    torch.cuda.synchronize(cuda_dev)
+    sa.device_status(cuda_dev)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        sa.plan_append(**s)
+    ws = api._default_ws_at[(cuda_dev.index, stream.cuda_stream)]
+    held = ws.buf.data_ptr()
+    with torch.cuda.stream(stream):
+        while ws.buf.data_ptr() == held:         # (it may have served larger calls before)
+            _grow(ws, cuda_dev, 2 * ws.buf.numel())
+        sa.sparse_decode_attn(c, q, sel, num_splits=64)
+        others = [torch.zeros(n, dtype=torch.uint8, device=cuda_dev) for n in (512, 768, 1024) * 8]
+    torch.cuda.synchronize(cuda_dev)
+    s["new_lens"].fill_(9)
+    graph.replay()
+    assert sa.device_status(cuda_dev) == (CAPACITY, (CAPACITY, 13, 27))
+    assert not any(bool(x.any()) for x in others)
+    del graph
