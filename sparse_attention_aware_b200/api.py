@@ -191,7 +191,9 @@ class Workspace:
     captured call was handed is kept instead: every replay of that graph writes
     to it again, and ``status`` reads it too.  A workspace that is captured must
     outlive its graphs; one that is made by a captured call is cleared by every
-    replay of that call's graph.
+    replay of that call's graph.  Graphs that share one are replayed one after the
+    other, unless their calls use its status word alone (``plan_append``,
+    ``rope_append``, ``expand_kv4``).
 
     What gives a call its address keeps the buffer as well, and the call holds it
     until it has launched: another thread's call on the same stream may replace

@@ -74,7 +74,7 @@
 // of 65536 tokens 139 us (0.56 by the 506 MB of distinct rows and lists; 794 MB are
 // read, since a row's 144 bytes touch 192 in 64-byte pieces and rows that heads share
 // come again, and by those it is 0.87); a masked step of 4 sequences 10 us, 256 of
-// 4096 tokens of 4 heads, fp32 queries, 5.1 us.  The copies alone take 67 and 134
+// 4096 tokens of 4 heads, fp32 queries, 5 us.  The copies alone take 67 and 134
 // us, the arithmetic alone 76 and 123: about 230 instructions per 16 rows (267 with
 // a list), of which widening the codes is a third, with 12 to 16 warps an SM.  Short
 // calls are bound by the dependent trips length -> entry -> page -> rows -> merge.
